@@ -58,6 +58,7 @@ def _log(rng, lo, hi):
 
 
 def draw(rng):
+    # blocks of up to 16 drafts: a state holds up to 64 query rows (block x heads per KV head) of a KV head
     op = rng.choice(["pages", "rows", "attend", "attend", "lora"])
     if op == "pages":
         if rng.random() < 0.5:
@@ -74,10 +75,10 @@ def draw(rng):
         heads = rng.choice(["qwen3", "qwen3", "mid", "narrow", "tiny"])
         batch = _log(rng, 1, 32)
         hi = _log(rng, 1, max(2, min(90000, 400000 // batch) if heads != "tiny" else 2000))
-        return dict(op="attend", heads=heads, batch=batch, rows=rng.choice([1, 1, 2, 5, 9, 17, 17, 33]),
+        return dict(op="attend", heads=heads, batch=batch, rows=rng.choice([1, 1, 2, 5, 9, 17, 17]),
                     lo=rng.randint(0, hi), hi=hi, page=rng.choice([16, 16, 32, 64, 128]))
     batch = _log(rng, 1, 48)
-    return dict(op="lora", batch=batch, block=rng.choice([1, 4, 8, 16, 16, 32]), layers=rng.randint(1, 4),
+    return dict(op="lora", batch=batch, block=rng.choice([1, 4, 8, 16, 16]), layers=rng.randint(1, 4),
                 hidden=rng.choice([512, 1024, 2560, 4096]), heads=rng.choice(["mid", "qwen3"]),
                 rank=rng.choice([8, 16, 24, 32, 64]), adapters=rng.randint(1, 24), share=rng.choice([0.0, 0.3]))
 
