@@ -29,6 +29,9 @@ LS_DEVERR_WAIT_TIMEOUT = 0x2
 LS_DEVERR_ORDER = 0x4
 LS_DEVERR_SAMPLE = 0x8
 LS_DEVERR_PAGE = 0x10
+LS_DEVERR_POOL = 0x20
+LS_DEVERR_ROWS = 0x40
+LS_DEVERR_ADAPTER = 0x80
 LS_MAX_PAGED_LAYERS = 64
 LS_F32 = 0
 LS_BF16 = 1
@@ -45,6 +48,8 @@ EXPORTED = (
     "ls_state_bytes", "ls_get_layout", "ls_init_state", "ls_prefill_workspace_bytes",
     "ls_prefill_summary", "ls_prefill_summary_noalloc", "ls_commit_round", "ls_draft_attend",
     "ls_draft_attend_views", "ls_view_state_bytes", "ls_round", "ls_accept_sampled", "ls_commit_accepted",
+    "ls_pages_extend", "ls_pages_trim", "ls_kv4_page_bytes", "ls_kv4_append", "ls_kv4_read_rows",
+    "ls_verify_workspace_bytes", "ls_verify_attend_kv4", "ls_lora_workspace_bytes", "ls_draft_prologue_lora",
     "ls_draft_prologue", "ls_prefill_paged", "ls_commit_round_paged", "ls_commit_accepted_paged", "ls_round_paged",
     "ls_clear_error", "ls_check_wait_timeout", "ls_round_overlaps", "ls_attend_uses_tensor_cores",
     "ls_read_state", "ls_get_error", "ls_destroy_state", "ls_status_string",
@@ -90,6 +95,58 @@ class ls_paged_kv(ctypes.Structure):
     ]
 
 
+class ls_page_pool(ctypes.Structure):
+    """Block tables, held counts and the stack of free pages that ls_pages_extend / ls_pages_trim
+    update in place."""
+    _fields_ = [
+        ("block_table", ctypes.c_void_p), ("held", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+        ("free_count", ctypes.c_void_p), ("max_blocks", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+    ]
+
+
+class ls_paged_kv4(ctypes.Structure):
+    """A paged KV cache held in 4 bits: per layer the base of its pages; page p of a layer at
+    base + p * page_stride bytes holds, per KV head, K codes, V codes, K scales, V scales."""
+    _fields_ = [
+        ("layers", ctypes.c_void_p * LS_MAX_PAGED_LAYERS), ("page_stride", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+    ]
+
+
+class ls_lora(ctypes.Structure):
+    """A bank of low-rank adapters of the two projections and each sequence's adapter id."""
+    _fields_ = [
+        ("a_q", ctypes.c_void_p), ("b_q", ctypes.c_void_p), ("a_kv", ctypes.c_void_p), ("b_kv", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p), ("adapter_of", ctypes.c_void_p), ("n_adapters", ctypes.c_int32),
+        ("rank", ctypes.c_int32),
+    ]
+
+
+def make_page_pool(block_table, held, free_pages, free_count, max_blocks, page_size, num_pages) -> ls_page_pool:
+    """Descriptor from int32 tensors (or addresses): [b][max_blocks], [b], [num_pages], [1]."""
+    return ls_page_pool(_ptr(block_table), _ptr(held), _ptr(free_pages), _ptr(free_count), max_blocks, page_size, num_pages)
+
+
+def make_paged_kv4(layers, page_stride, block_table, max_blocks, page_size, num_pages) -> ls_paged_kv4:
+    """Descriptor from per-layer page buffers (tensors or addresses; page_stride in bytes) and an
+    int32 block table (None where only rows are written and read by slot)."""
+    if len(layers) > LS_MAX_PAGED_LAYERS:
+        raise ValueError("one page buffer per layer, at most LS_MAX_PAGED_LAYERS")
+    kv = ls_paged_kv4()
+    for l, x in enumerate(layers):
+        kv.layers[l] = _ptr(x)
+    kv.page_stride, kv.block_table = page_stride, _ptr(block_table)
+    kv.max_blocks, kv.page_size, kv.num_pages = max_blocks, page_size, num_pages
+    return kv
+
+
+def make_lora(n_adapters, rank, a_q, b_q, a_kv, b_kv, scale, adapter_of) -> ls_lora:
+    """Descriptor of an adapter bank (tensors or addresses) and the int32 adapter id per sequence."""
+    return ls_lora(_ptr(a_q), _ptr(b_q), _ptr(a_kv), _ptr(b_kv), _ptr(scale), _ptr(adapter_of), n_adapters, rank)
+
+
 def make_paged_kv(k_layers, v_layers, page_stride, slot_stride, block_table, max_blocks, page_size,
                   num_pages, verify_slots=None) -> ls_paged_kv:
     """Descriptor from per-layer page buffers (tensors or addresses), an int32 block table and,
@@ -114,7 +171,17 @@ def _load():
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     cfgp = ctypes.POINTER(ls_config)
     pkvp = ctypes.POINTER(ls_paged_kv)
+    poolp, kv4p, lorap = ctypes.POINTER(ls_page_pool), ctypes.POINTER(ls_paged_kv4), ctypes.POINTER(ls_lora)
     sig = {
+        "ls_pages_extend": (ctypes.c_int, [vp, poolp, vp, vp, i32, vp, vp, i64, vp]),
+        "ls_pages_trim": (ctypes.c_int, [vp, poolp, vp, vp]),
+        "ls_kv4_page_bytes": (sz, [cfgp, i32]),
+        "ls_kv4_append": (ctypes.c_int, [vp, kv4p, i32, vp, vp, i64, vp, i64, vp]),
+        "ls_kv4_read_rows": (ctypes.c_int, [vp, kv4p, i32, vp, i64, vp, vp, i64, vp]),
+        "ls_verify_workspace_bytes": (sz, [cfgp, i32]),
+        "ls_verify_attend_kv4": (ctypes.c_int, [vp, kv4p, i32, vp, i64, i32, vp, vp, ctypes.c_float, vp, vp, sz, vp]),
+        "ls_lora_workspace_bytes": (sz, [cfgp, i32]),
+        "ls_draft_prologue_lora": (ctypes.c_int, [vp, vp, vp, vp, lorap, vp, vp, vp, sz, vp]),
         "ls_prefill_paged": (ctypes.c_int, [vp, pkvp, vp, i64, i64, vp, vp, sz, vp]),
         "ls_commit_round_paged": (ctypes.c_int, [vp, vp, vp, pkvp, vp, vp, vp, vp]),
         "ls_commit_accepted_paged": (ctypes.c_int, [vp, vp, pkvp, vp, vp]),
@@ -310,6 +377,56 @@ def ls_round_paged(state, draft_ids, target_ids, kv: ls_paged_kv, verify_hidden,
         state, _ptr(draft_ids), _ptr(target_ids), ctypes.byref(kv), _ptr(verify_hidden), _ptr(accept_len),
         _ptr(next_token), _ptr(q), boundary_k_offset, boundary_v_offset, float(softmax_scale), _ptr(out),
         _stream(stream)))
+
+
+def ls_pages_extend(state, pool: ls_page_pool, length, rows, max_rows, row_begin, slots, slot_capacity,
+                    stream=None) -> None:
+    """Pages and slots of every sequence's next rows; length None: the state's own lengths."""
+    _check("ls_pages_extend", _lib.ls_pages_extend(
+        state, ctypes.byref(pool), _ptr(length), _ptr(rows), max_rows, _ptr(row_begin), _ptr(slots), slot_capacity,
+        _stream(stream)))
+
+
+def ls_pages_trim(state, pool: ls_page_pool, length, stream=None) -> None:
+    """Pages behind every sequence's rows go back to the free list; length None: the state's own."""
+    _check("ls_pages_trim", _lib.ls_pages_trim(state, ctypes.byref(pool), _ptr(length), _stream(stream)))
+
+
+def ls_kv4_page_bytes(cfg: ls_config, page_size: int) -> int:
+    return int(_lib.ls_kv4_page_bytes(ctypes.byref(cfg), page_size))
+
+
+def ls_kv4_append(state, kv: ls_paged_kv4, layer, k, v, row_stride, slots, n_rows, stream=None) -> None:
+    _check("ls_kv4_append", _lib.ls_kv4_append(
+        state, ctypes.byref(kv), layer, _ptr(k), _ptr(v), row_stride, _ptr(slots), n_rows, _stream(stream)))
+
+
+def ls_kv4_read_rows(state, kv: ls_paged_kv4, layer, slots, n_rows, k, v, row_stride, stream=None) -> None:
+    _check("ls_kv4_read_rows", _lib.ls_kv4_read_rows(
+        state, ctypes.byref(kv), layer, _ptr(slots), n_rows, _ptr(k), _ptr(v), row_stride, _stream(stream)))
+
+
+def ls_verify_workspace_bytes(cfg: ls_config, n_rows: int) -> int:
+    return int(_lib.ls_verify_workspace_bytes(ctypes.byref(cfg), n_rows))
+
+
+def ls_verify_attend_kv4(state, kv: ls_paged_kv4, layer, q, q_stride, n_rows, rows, kv_len, softmax_scale, out,
+                         workspace, workspace_bytes, stream=None) -> None:
+    """Attention of every sequence's last n_rows rows over its 4-bit cache."""
+    _check("ls_verify_attend_kv4", _lib.ls_verify_attend_kv4(
+        state, ctypes.byref(kv), layer, _ptr(q), q_stride, n_rows, _ptr(rows), _ptr(kv_len), float(softmax_scale),
+        _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def ls_lora_workspace_bytes(cfg: ls_config, rank: int) -> int:
+    return int(_lib.ls_lora_workspace_bytes(ctypes.byref(cfg), rank))
+
+
+def ls_draft_prologue_lora(state, w_kv, w_q, x, lora: ls_lora, bkv, q, workspace, workspace_bytes, stream=None) -> None:
+    """The projections with each sequence's own low-rank adapter."""
+    _check("ls_draft_prologue_lora", _lib.ls_draft_prologue_lora(
+        state, _ptr(w_kv), _ptr(w_q), _ptr(x), ctypes.byref(lora), _ptr(bkv), _ptr(q), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
 
 
 def ls_round_overlaps(state) -> bool:

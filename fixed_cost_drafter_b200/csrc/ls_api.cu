@@ -12,8 +12,22 @@ cudaError_t launch_commit(const Dev& p, const int32_t* draft, const int32_t* tar
                           const void* vv, const void* vh, int32_t* accept_len, int32_t* next_token,
                           const int32_t* given_a, cudaStream_t stream);
 bool prologue_supported(const Dev& p);
-cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, const void* x, void* bkv, void* q,
-                            int sms, cudaStream_t stream);
+cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, const void* x, const ls_lora* lora,
+                            void* low, void* bkv, void* q, int sms, cudaStream_t stream);
+size_t lora_workspace_bytes(const ls_config& c, int rank);
+cudaError_t launch_pages_extend(const Dev& p, const ls_page_pool& pool, const int64_t* len, const int32_t* rows,
+                                int max_rows, int64_t* row_begin, int64_t* slots, int64_t capacity, int sms,
+                                cudaStream_t stream);
+cudaError_t launch_pages_trim(const Dev& p, const ls_page_pool& pool, const int64_t* len, int sms,
+                              cudaStream_t stream);
+cudaError_t launch_kv4_append(const Dev& p, const ls_paged_kv4& kv, int layer, const void* k, const void* v,
+                              int64_t row_stride, const int64_t* slots, int64_t n_rows, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Dev& p, const ls_paged_kv4& kv, int layer, const int64_t* slots, int64_t n_rows,
+                            void* k, void* v, int64_t row_stride, cudaStream_t stream);
+size_t verify_workspace_bytes(const ls_config& c, int n_rows);
+cudaError_t launch_verify(const Dev& p, const ls_config& c, const ls_paged_kv4& kv, int layer, const void* q,
+                          int64_t q_stride, int n_rows, const int32_t* rows, const int64_t* kv_len, float scale,
+                          void* out, void* ws, int sms, cudaStream_t stream);
 cudaError_t launch_sample(const Dev& p, const int32_t* draft, const float* q, const float* pr, int vocab,
                           const float* u, int32_t* accept_len, int32_t* next_token, cudaStream_t stream);
 bool simt_supported(const Dev& p);
@@ -126,6 +140,49 @@ int validate_paged(const ls_config& c, const ls_paged_kv* kv) {
       kv->page_stride < 0 || kv->page_stride % 8 != 0)
     return LS_ERR_SHAPE;
   return LS_OK;
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int validate_pool(const ls_page_pool* pool) {
+  if (!pool || !pool->block_table || !pool->held || !pool->free_pages || !pool->free_count) return LS_ERR_INVALID_ARG;
+  if (!aligned(pool->block_table, 4) || !aligned(pool->held, 4) || !aligned(pool->free_pages, 4) ||
+      !aligned(pool->free_count, 4))
+    return LS_ERR_INVALID_ARG;
+  if (pool->max_blocks < 1 || pool->page_size < 1 || pool->num_pages < 1) return LS_ERR_INVALID_ARG;
+  return pool->num_pages > INT32_MAX ? LS_ERR_UNSUPPORTED : LS_OK;
+}
+
+bool kv4_shapes_ok(const ls_config& c, int page_size) {
+  return (c.head_dim == 64 || c.head_dim == 128) && pow2(page_size) && page_size >= 16 && page_size <= 256;
+}
+
+// A 4-bit cache usable by the kernels for this config, and its layer `layer`.
+int validate_kv4(const ls_config& c, const ls_paged_kv4* kv, int layer, bool table) {
+  if (!kv) return LS_ERR_INVALID_ARG;
+  if (c.n_layers > LS_MAX_PAGED_LAYERS) return LS_ERR_UNSUPPORTED;
+  if (layer < 0 || layer >= c.n_layers) return LS_ERR_INVALID_ARG;
+  if (!kv->layers[layer] || !aligned16(kv->layers[layer])) return LS_ERR_INVALID_ARG;
+  if (kv->page_size < 1 || kv->num_pages < 1) return LS_ERR_INVALID_ARG;
+  if (table && (!kv->block_table || !aligned(kv->block_table, 4) || kv->max_blocks < 1)) return LS_ERR_INVALID_ARG;
+  if (!kv4_shapes_ok(c, kv->page_size)) return LS_ERR_UNSUPPORTED;
+  if (kv->page_stride % 16 != 0 || kv->page_stride < int64_t(ls_kv4_page_bytes(&c, kv->page_size)))
+    return LS_ERR_SHAPE;
+  // page ids are int32, and the last page's end has to be an address
+  if (kv->num_pages > INT32_MAX || kv->page_stride > INT64_MAX / (int64_t(1) << 32)) return LS_ERR_UNSUPPORTED;
+  return LS_OK;
+}
+
+int rows_checks(const ls_state* st, const ls_paged_kv4* kv, int layer, const void* k, const void* v,
+                int64_t row_stride, const int64_t* slots, int64_t n_rows) {
+  const ls_config& c = st->cfg;
+  const int r = validate_kv4(c, kv, layer, false);
+  if (r != LS_OK) return r;
+  if (n_rows < 0) return LS_ERR_INVALID_ARG;
+  if (n_rows == 0) return LS_OK;
+  if (!k || !v || !slots || !aligned16(k) || !aligned16(v) || !aligned(slots, 8)) return LS_ERR_INVALID_ARG;
+  if (row_stride < int64_t(c.n_kv_heads) * c.head_dim || row_stride % 8 != 0) return LS_ERR_SHAPE;
+  return n_rows > INT64_MAX / 8 / row_stride ? LS_ERR_UNSUPPORTED : LS_OK;
 }
 
 // Argument checks of the whole-round calls beyond those of the commit they make.
@@ -405,7 +462,118 @@ int ls_draft_prologue(const ls_state* st, const void* d_w_kv, const void* d_w_q,
   if (!ls::prologue_supported(st->dev)) return LS_ERR_UNSUPPORTED;
   if (!aligned16(d_w_kv) || !aligned16(d_w_q) || !aligned16(d_x) || !aligned16(d_bkv) || !aligned16(d_q))
     return LS_ERR_INVALID_ARG;
-  const cudaError_t e = ls::launch_prologue(st->dev, d_w_kv, d_w_q, d_x, d_bkv, d_q, st->sms, stream);
+  const cudaError_t e = ls::launch_prologue(st->dev, d_w_kv, d_w_q, d_x, nullptr, nullptr, d_bkv, d_q, st->sms, stream);
+  if (e == cudaSuccess) mark_settled(st, stream);
+  return e == cudaErrorNotSupported ? LS_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+size_t ls_lora_workspace_bytes(const ls_config* cfg, int32_t rank) {
+  if (validate(cfg) != LS_OK || rank < 8 || rank > 128 || rank % 8 != 0) return 0;
+  return ls::lora_workspace_bytes(*cfg, rank);
+}
+
+int ls_draft_prologue_lora(const ls_state* st, const void* d_w_kv, const void* d_w_q, const void* d_x,
+                           const ls_lora* h_lora, void* d_bkv, void* d_q, void* d_workspace, size_t workspace_bytes,
+                           cudaStream_t stream) {
+  if (!st || !d_w_kv || !d_w_q || !d_x || !h_lora || !d_bkv || !d_q || !d_workspace) return LS_ERR_INVALID_ARG;
+  if (!on_state_device(st)) return LS_ERR_INVALID_ARG;
+  if (!ls::prologue_supported(st->dev)) return LS_ERR_UNSUPPORTED;
+  const ls_lora& lo = *h_lora;
+  if (!lo.a_q || !lo.b_q || !lo.a_kv || !lo.b_kv || !lo.scale || !lo.adapter_of || lo.n_adapters < 1)
+    return LS_ERR_INVALID_ARG;
+  if (lo.rank < 8 || lo.rank > 128 || lo.rank % 8 != 0) return LS_ERR_UNSUPPORTED;
+  if (!aligned16(lo.a_q) || !aligned16(lo.b_q) || !aligned16(lo.a_kv) || !aligned16(lo.b_kv) ||
+      !aligned16(lo.scale) || !aligned16(lo.adapter_of))
+    return LS_ERR_INVALID_ARG;
+  if (!aligned16(d_w_kv) || !aligned16(d_w_q) || !aligned16(d_x) || !aligned16(d_bkv) || !aligned16(d_q) ||
+      !aligned(d_workspace, 256))
+    return LS_ERR_INVALID_ARG;
+  if (workspace_bytes < ls::lora_workspace_bytes(st->cfg, lo.rank)) return LS_ERR_SHAPE;
+  const cudaError_t e = ls::launch_prologue(st->dev, d_w_kv, d_w_q, d_x, h_lora, d_workspace, d_bkv, d_q, st->sms,
+                                            stream);
+  if (e == cudaSuccess) mark_settled(st, stream);
+  return e == cudaErrorNotSupported ? LS_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+int ls_pages_extend(ls_state* st, const ls_page_pool* h_pool, const int64_t* d_len, const int32_t* d_rows,
+                    int32_t max_rows, int64_t* d_row_begin, int64_t* d_slots, int64_t slot_capacity,
+                    cudaStream_t stream) {
+  if (!st || max_rows < 0 || slot_capacity < 0) return LS_ERR_INVALID_ARG;
+  if (!on_state_device(st)) return LS_ERR_INVALID_ARG;
+  const int v = validate_pool(h_pool);
+  if (v != LS_OK) return v;
+  if (slot_capacity > 0 && !d_slots) return LS_ERR_INVALID_ARG;
+  if (!aligned(d_len, 8) || !aligned(d_rows, 4) || !aligned(d_row_begin, 8) || !aligned(d_slots, 8))
+    return LS_ERR_INVALID_ARG;
+  if (!d_row_begin && slot_capacity < int64_t(st->cfg.batch) * max_rows) return LS_ERR_SHAPE;
+  const int r = cuda_status(ls::launch_pages_extend(st->dev, *h_pool, d_len, d_rows, max_rows, d_row_begin, d_slots,
+                                                    slot_capacity, st->sms, stream));
+  if (r == LS_OK) mark_settled(st, stream);
+  return r;
+}
+
+int ls_pages_trim(ls_state* st, const ls_page_pool* h_pool, const int64_t* d_len, cudaStream_t stream) {
+  if (!st) return LS_ERR_INVALID_ARG;
+  if (!on_state_device(st)) return LS_ERR_INVALID_ARG;
+  const int v = validate_pool(h_pool);
+  if (v != LS_OK) return v;
+  if (!aligned(d_len, 8)) return LS_ERR_INVALID_ARG;
+  const int r = cuda_status(ls::launch_pages_trim(st->dev, *h_pool, d_len, st->sms, stream));
+  if (r == LS_OK) mark_settled(st, stream);
+  return r;
+}
+
+size_t ls_kv4_page_bytes(const ls_config* cfg, int32_t page_size) {
+  if (validate(cfg) != LS_OK || !kv4_shapes_ok(*cfg, page_size)) return 0;
+  return size_t(cfg->n_kv_heads) * page_size * (cfg->head_dim + cfg->head_dim / 8);
+}
+
+int ls_kv4_append(ls_state* st, const ls_paged_kv4* h_kv, int32_t layer, const void* d_k, const void* d_v,
+                  int64_t row_stride, const int64_t* d_slots, int64_t n_rows, cudaStream_t stream) {
+  if (!st) return LS_ERR_INVALID_ARG;
+  if (!on_state_device(st)) return LS_ERR_INVALID_ARG;
+  const int v = rows_checks(st, h_kv, layer, d_k, d_v, row_stride, d_slots, n_rows);
+  if (v != LS_OK || n_rows == 0) return v;
+  const cudaError_t e = ls::launch_kv4_append(st->dev, *h_kv, layer, d_k, d_v, row_stride, d_slots, n_rows, stream);
+  if (e == cudaSuccess) mark_settled(st, stream);
+  return e == cudaErrorNotSupported ? LS_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+int ls_kv4_read_rows(ls_state* st, const ls_paged_kv4* h_kv, int32_t layer, const int64_t* d_slots, int64_t n_rows,
+                     void* d_k, void* d_v, int64_t row_stride, cudaStream_t stream) {
+  if (!st) return LS_ERR_INVALID_ARG;
+  if (!on_state_device(st)) return LS_ERR_INVALID_ARG;
+  const int v = rows_checks(st, h_kv, layer, d_k, d_v, row_stride, d_slots, n_rows);
+  if (v != LS_OK || n_rows == 0) return v;
+  const cudaError_t e = ls::launch_kv4_read(st->dev, *h_kv, layer, d_slots, n_rows, d_k, d_v, row_stride, stream);
+  if (e == cudaSuccess) mark_settled(st, stream);
+  return e == cudaErrorNotSupported ? LS_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+size_t ls_verify_workspace_bytes(const ls_config* cfg, int32_t n_rows) {
+  if (validate(cfg) != LS_OK || n_rows < 1 || n_rows > cfg->block + 1) return 0;
+  if (cfg->head_dim != 64 && cfg->head_dim != 128) return 0;
+  return ls::verify_workspace_bytes(*cfg, n_rows);
+}
+
+int ls_verify_attend_kv4(const ls_state* st, const ls_paged_kv4* h_kv, int32_t layer, const void* d_q,
+                         int64_t q_stride, int32_t n_rows, const int32_t* d_rows, const int64_t* d_kv_len,
+                         float softmax_scale, void* d_out, void* d_workspace, size_t workspace_bytes,
+                         cudaStream_t stream) {
+  if (!st || !d_q || !d_kv_len || !d_out || !d_workspace) return LS_ERR_INVALID_ARG;
+  if (!on_state_device(st)) return LS_ERR_INVALID_ARG;
+  const ls_config& c = st->cfg;
+  const int v = validate_kv4(c, h_kv, layer, true);
+  if (v != LS_OK) return v;
+  if (n_rows < 1) return LS_ERR_INVALID_ARG;
+  if (n_rows > c.block + 1 || q_stride < int64_t(c.n_q_heads) * c.head_dim || q_stride % 8 != 0) return LS_ERR_SHAPE;
+  if (!(softmax_scale > 0.0f) || softmax_scale == INFINITY) return LS_ERR_INVALID_ARG;
+  if (!aligned16(d_q) || !aligned16(d_out) || !aligned(d_workspace, 256) || !aligned(d_rows, 4) ||
+      !aligned(d_kv_len, 8))
+    return LS_ERR_INVALID_ARG;
+  if (workspace_bytes < ls::verify_workspace_bytes(c, n_rows)) return LS_ERR_SHAPE;
+  const cudaError_t e = ls::launch_verify(st->dev, c, *h_kv, layer, d_q, q_stride, n_rows, d_rows, d_kv_len,
+                                          softmax_scale, d_out, d_workspace, st->sms, stream);
   if (e == cudaSuccess) mark_settled(st, stream);
   return e == cudaErrorNotSupported ? LS_ERR_UNSUPPORTED : cuda_status(e);
 }

@@ -75,6 +75,13 @@ struct PArgs {
   int32_t* err;
 };
 
+// Low-rank adapters (ls_draft_prologue_lora): low[p] holds scale * (A x) of problem p in fp32,
+// [b][L][rows_per_seq][rank], 0 for a sequence without an adapter.
+struct PLora {
+  ls_lora bank;
+  float* low[2];
+};
+
 struct PBars {
   uint64_t afull[kPAStages], aempty[kPAStages];  // per k-step k: stage k mod kPAStages of
                                                  // both rings full (2 arrivals) / released
@@ -170,8 +177,9 @@ __device__ inline bool pwait(PBars& s, uint64_t* bar, uint32_t parity, int32_t* 
   return false;
 }
 
+template <bool kLora>
 __global__ void __launch_bounds__(kPThreads, 1)
-prologue_kernel(const PArgs a, const __grid_constant__ CUtensorMap w0, const __grid_constant__ CUtensorMap x0,
+prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtensorMap w0, const __grid_constant__ CUtensorMap x0,
                 const __grid_constant__ CUtensorMap w1, const __grid_constant__ CUtensorMap x1) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ PBars s;
@@ -307,6 +315,28 @@ prologue_kernel(const PArgs a, const __grid_constant__ CUtensorMap w0, const __g
       mbar_arrive(&s.epi);
       return __all_sync(0xffffffffu, pwait(s, &s.epi, uint32_t(meets++) & 1, a.err));
     };
+    // the adapters' part of this thread's weight row, activation rows col .. col + n - 1
+    auto add_low = [&](const PUnit& u, const PProblem& P, int col, int n, float (&v)[32]) {
+      const int R = lora.bank.rank;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        if (j >= n) break;
+        const int m = col + j, sq = u.mt * P.seq_per_unit + m / P.rows_per_seq, r = m % P.rows_per_seq;
+        const int ad = lora.bank.adapter_of[sq];
+        if (ad < 0 || ad >= lora.bank.n_adapters) continue;
+        const float* h = lora.low[u.p] + ((int64_t(sq) * a.L + u.l) * P.rows_per_seq + r) * R;
+        const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(u.p ? lora.bank.b_kv : lora.bank.b_q) +
+                                 ((int64_t(ad) * a.L + u.l) * P.n_out + u.nt * kPTileN + ecol) * R;
+        float x = 0.f;
+        for (int e = 0; e < R; e += 8) {
+          float f[8];
+          Elem<__nv_bfloat16>::to_f32(ld_nc_v4(w + e), f);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) x = fmaf(f[q], h[e + q], x);
+        }
+        v[j] += x;
+      }
+    };
     auto store_tile = [&](const PUnit& u, const PProblem& P, auto&& fetch) -> bool {
       const int seq0 = u.mt * P.seq_per_unit;
       const int rows = min(P.seq_per_unit, a.b - seq0) * P.rows_per_seq;  // valid activation rows
@@ -317,6 +347,7 @@ prologue_kernel(const PArgs a, const __grid_constant__ CUtensorMap w0, const __g
         for (int c0 = 0; c0 < nr; c0 += 32) {
           float v[32];
           fetch(r0 + c0, v);
+          if constexpr (kLora) add_low(u, P, r0 + c0, min(32, rows - r0 - c0), v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) stage[(c0 + j) * kPTileN + ecol] = __float2bfloat16_rn(v[j]);
         }
@@ -414,6 +445,51 @@ prologue_kernel(const PArgs a, const __grid_constant__ CUtensorMap w0, const __g
   }
 }
 
+// low[p][b][l][row][r] = scale (A x): a warp per r of a (sequence, layer), up to 16 rows at a time.
+__global__ void __launch_bounds__(256) lora_low_kernel(const PLora lora, const __nv_bfloat16* x,
+                                                       const __nv_bfloat16* boundary, int L, int B, int hidden,
+                                                       int32_t* err) {
+  const int b = int(blockIdx.x) / L, l = int(blockIdx.x) - b * L, p = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = lora.bank.rank;
+  const int rows = p ? 1 : B;
+  const int ad = lora.bank.adapter_of[b];
+  const bool none = ad < 0 || ad >= lora.bank.n_adapters;
+  if (none && ad != -1 && threadIdx.x == 0) set_err(err, LS_DEVERR_ADAPTER);
+  const __nv_bfloat16* src = p ? boundary + (int64_t(b) * L + l) * hidden : x + (int64_t(b) * L + l) * B * hidden;
+  float* low = lora.low[p] + (int64_t(b) * L + l) * rows * R;
+  const float scale = none ? 0.f : lora.bank.scale[ad];
+  for (int r = warp; r < R; r += 8) {
+    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p ? lora.bank.a_kv : lora.bank.a_q) +
+                             ((int64_t(none ? 0 : ad) * L + l) * R + r) * hidden;
+    for (int i0 = 0; i0 < rows; i0 += 16) {
+      float acc[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+      if (!none) {
+        for (int k = lane * 8; k < hidden; k += 256) {
+          float f[8];
+          Elem<__nv_bfloat16>::to_f32(ld_nc_v4(w + k), f);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (i0 + i >= rows) break;
+            float g[8];
+            Elem<__nv_bfloat16>::to_f32(ld_nc_v4(src + int64_t(i0 + i) * hidden + k), g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[i] = fmaf(f[e], g[e], acc[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i0 + i >= rows) break;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+        if (lane == 0) low[int64_t(i0 + i) * R + r] = none ? 0.f : scale * acc[i];
+      }
+    }
+  }
+}
+
 bool encode_bf16(void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
                  CUtensorMap* out) {
   EncodeTiledFn fn = encode_fn();
@@ -428,10 +504,15 @@ bool encode_bf16(void* base, int rank, const cuuint64_t* dims, const cuuint64_t*
 
 bool prologue_supported(const Dev& p) { return prologue_shapes_ok(p.dtype, p.hidden, p.Hq, p.Hkv, p.D, p.B); }
 
-cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, const void* x, void* bkv, void* q,
-                            int sms, cudaStream_t stream) {
+size_t lora_workspace_bytes(const ls_config& c, int rank) {
+  return size_t(align256(int64_t(c.batch) * c.n_layers * (c.block + 1) * rank * 4));
+}
+
+cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, const void* x, const ls_lora* lora,
+                            void* low, void* bkv, void* q, int sms, cudaStream_t stream) {
+  const auto kernel = lora ? prologue_kernel<true> : prologue_kernel<false>;
   // per launch: the attribute belongs to the current device's copy of the kernel
-  cudaError_t e = cudaFuncSetAttribute(prologue_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmemBytes);
   if (e != cudaSuccess) return e;
   PArgs a{};
   a.b = p.b;
@@ -489,6 +570,17 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
     const cuuint32_t box[3] = {kPKStep, 1, cuuint32_t(K.load_rows)};
     if (!encode_bf16(p.boundary, 3, dims, str, box, &mx1)) return cudaErrorInvalidValue;
   }
+  PLora pl{};
+  if (lora) {
+    pl.bank = *lora;
+    pl.low[0] = static_cast<float*>(low);
+    pl.low[1] = pl.low[0] + int64_t(p.b) * p.L * p.B * lora->rank;
+    lora_low_kernel<<<dim3(p.b * p.L, 2), 256, 0, stream>>>(pl, static_cast<const __nv_bfloat16*>(x),
+                                                            reinterpret_cast<const __nv_bfloat16*>(p.boundary), p.L,
+                                                            p.B, p.hidden, p.err);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   int grid = sms < kProMaxGrid ? sms : kProMaxGrid;
   if (a.n_units < grid) grid = a.n_units;
   // units left over after whole waves: split their k-steps over every CTA when they are all
@@ -514,7 +606,7 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prologue_kernel, a, mw0, mx0, mw1, mx1);
+  return cudaLaunchKernelEx(&cfg, kernel, a, pl, mw0, mx0, mw1, mx1);
 }
 
 }  // namespace ls

@@ -1,0 +1,182 @@
+// Shared by the kernels of ls_verify_attend_kv4: arguments, the split of the work over the
+// CTAs and where partial results go.
+//
+// Work: a tile is (sequence, KV head, block of MR query rows); row m of a (sequence, KV head)
+// is query row m / group of query head g * group + m mod group. A tile's keys come in chunks
+// of 128. All tiles' chunks form one line (sequence by sequence), cut into G equal ranges, one
+// per CTA, whatever the lengths are: no CTA has more than one chunk more than another. A CTA
+// whose range holds a whole tile writes its output rows; the pieces of a tile that is cut
+// leave (reference, sum, unscaled output) in fp32, and a second kernel joins them in range
+// order, so repeated calls give the same bits.
+#pragma once
+#include "ls_kv4.cuh"
+
+namespace ls {
+
+constexpr int kVerChunk = 128;   // keys per chunk
+constexpr int kVerMaxSms = 160;  // CTA slots are sized for at most this many SMs
+constexpr int kSimtRows = 8;     // MR of the CUDA-core kernel
+constexpr int kSimtCtas = 4;     // its CTAs per SM
+
+struct VerArgs {
+  const unsigned char* base;  // the layer's pages
+  int64_t page_stride, num_pages;
+  const int32_t* table;
+  int32_t max_blocks, page_size, page_shift;
+  const void* q;
+  int64_t q_stride;
+  int32_t n_rows;
+  const int32_t* rows;
+  const int64_t* kv_len;
+  float scale_log2;  // softmax_scale * log2(e)
+  void* out;
+  float* part_ml;  // [2 G][MR][2]: reference (log2 units) and sum of a piece's rows
+  float* part_o;   // [2 G][MR][D]
+  int32_t b, Hkv, Hq, grp, D;
+  int32_t M, MR, HM;  // rows per (sequence, KV head), rows per tile, tiles per sequence
+  int32_t G;          // CTAs
+  int32_t out_f32, f32_in;
+  int32_t* err;
+};
+
+__device__ inline int64_t ver_len(const VerArgs& a, int b) {
+  const int64_t n = a.kv_len[b];
+  return n < 0 || n > int64_t(a.max_blocks) * a.page_size ? 0 : n;
+}
+__device__ inline int ver_rows(const VerArgs& a, int b) {
+  if (!a.rows) return a.n_rows;
+  const int n = a.rows[b];
+  return n < 0 ? 0 : (n > a.n_rows ? a.n_rows : n);
+}
+__device__ inline int64_t ver_chunks(const VerArgs& a, int b) { return (ver_len(a, b) + kVerChunk - 1) / kVerChunk; }
+
+__device__ inline int64_t ver_warp_sum(int64_t x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Chunks of one tile row of the sequences [0, upto), whole warp.
+__device__ inline int64_t ver_chunks_before(const VerArgs& a, int upto) {
+  int64_t x = 0;
+  for (int i = int(threadIdx.x & 31); i < upto; i += 32) x += ver_chunks(a, i);
+  return ver_warp_sum(x);
+}
+
+// A CTA's place in the line of chunks.
+struct VerCursor {
+  int b, hm;      // next piece: sequence, tile of it
+  int64_t chunk;  // its first chunk
+  int64_t left;   // chunks left in this CTA's range
+};
+
+// One piece of a tile: chunks [c0, c1) of n.
+struct VerPiece {
+  int b, hm, rows;
+  int64_t c0, c1, n, len;
+};
+
+// Whole warp. total: chunks of all tiles.
+__device__ inline VerCursor ver_begin(const VerArgs& a, int cta) {
+  VerCursor u{0, 0, 0, 0};
+  const int lane = threadIdx.x & 31;
+  const int64_t T = ver_chunks_before(a, a.b) * a.HM;
+  const int64_t G = T < a.G ? T : a.G;
+  if (cta >= G) return u;
+  const int64_t g0 = int64_t(cta) * T / G, g1 = int64_t(cta + 1) * T / G;
+  u.left = g1 - g0;
+  int64_t base = 0;  // chunks of the sequences before the 32 looked at
+  for (int i0 = 0; i0 < a.b; i0 += 32) {
+    const int64_t mine = i0 + lane < a.b ? ver_chunks(a, i0 + lane) * a.HM : 0;
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + inc > g0);
+    if (hit) {
+      const int w = __ffs(int(hit)) - 1;
+      const int64_t n = __shfl_sync(0xffffffffu, mine, w) / a.HM;
+      const int64_t r = g0 - base - __shfl_sync(0xffffffffu, inc - mine, w);
+      u.b = i0 + w;
+      u.hm = int(r / n);
+      u.chunk = r - int64_t(u.hm) * n;
+      return u;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  u.left = 0;  // not reached: g0 < T
+  return u;
+}
+
+__device__ inline bool ver_next(const VerArgs& a, VerCursor& u, VerPiece& p) {
+  if (u.left <= 0) return false;
+  while (u.b < a.b) {
+    p.len = ver_len(a, u.b);
+    p.n = (p.len + kVerChunk - 1) / kVerChunk;
+    if (p.n > 0) break;
+    ++u.b;
+  }
+  if (u.b >= a.b) return false;
+  p.b = u.b;
+  p.hm = u.hm;
+  p.rows = ver_rows(a, u.b);
+  p.c0 = u.chunk;
+  p.c1 = p.n - p.c0 < u.left ? p.n : p.c0 + u.left;
+  u.left -= p.c1 - p.c0;
+  u.chunk = 0;
+  if (++u.hm == a.HM) {
+    u.hm = 0;
+    ++u.b;
+  }
+  return true;
+}
+
+// The slot of a cut tile's piece: a CTA cuts at most the tile its range begins in and the one
+// it ends in.
+__device__ inline int ver_slot(int cta, const VerPiece& p) { return 2 * cta + (p.c0 == 0 ? 1 : 0); }
+
+// Keys that query row i of the piece's sequence sees: positions [0, limit).
+__device__ inline int64_t ver_limit(const VerPiece& p, int i) {
+  const int64_t t = p.len - p.rows + i + 1;
+  return t < 0 ? 0 : t;
+}
+
+// Base of the (page, KV head) block of the page at index pi of sequence b; a page id outside
+// the pool is flagged and read as page 0.
+__device__ inline const unsigned char* ver_block(const VerArgs& a, int b, int64_t pi, int head) {
+  int64_t page = __ldg(a.table + int64_t(b) * a.max_blocks + pi);
+  if (page < 0 || page >= a.num_pages) {
+    set_err(a.err, LS_DEVERR_PAGE);
+    page = 0;
+  }
+  return a.base + page * a.page_stride + int64_t(head) * kv4_block_bytes(a.page_size, a.D);
+}
+
+// A value group with a NaN scale makes the rows that see its key NaN, and only those: weights
+// of unseen keys are 0, and 0 * NaN would reach the others. Such a group takes part as zeros,
+// and the smallest position per group of 16 elements is kept here (per piece): a row's group
+// is NaN if its limit lies behind that position.
+constexpr int kVerNone = 0x7fffffff;
+__device__ inline bool nan_scale(uint32_t byte) { return (byte & 0x7fu) == 0x7fu; }
+
+// N output elements to memory, N a multiple of 2.
+template <int N>
+__device__ inline void ver_store(const VerArgs& a, int64_t at, const float* v) {
+  if (a.out_f32 || a.f32_in) {
+    float* o = static_cast<float*>(a.out) + at;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) *reinterpret_cast<float2*>(o + j) = make_float2(v[j], v[j + 1]);
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) *reinterpret_cast<__nv_bfloat162*>(o + j) = __floats2bfloat162_rn(v[j], v[j + 1]);
+  }
+}
+// Where row i, query head h of sequence b starts in the output.
+__device__ inline int64_t ver_out_at(const VerArgs& a, int b, int i, int h) {
+  return ((int64_t(b) * a.n_rows + i) * a.Hq + h) * a.D;
+}
+
+}  // namespace ls

@@ -80,6 +80,13 @@ extern "C" {
 #define LS_DEVERR_PAGE        0x10  /* paged calls: a position past the block table's
                                        max_blocks pages or a page id outside
                                        [0, num_pages) (the rows are read from page 0)  */
+#define LS_DEVERR_POOL        0x20  /* ls_pages_extend: the free list holds too few pages for
+                                       a sequence; ls_pages_extend / ls_pages_trim: counts
+                                       that contradict each other (see there)           */
+#define LS_DEVERR_ROWS        0x40  /* a sequence's row count, length or held page count
+                                       outside its range (ls_pages_*, ls_verify_attend_kv4) */
+#define LS_DEVERR_ADAPTER     0x80  /* an adapter id outside [-1, n_adapters) (the sequence
+                                       is projected without an adapter)                 */
 
 /* ---- views (Figure 2 caption (b); the component ablations of Table 5) -------- */
 #define LS_VIEW_BOUNDARY 0x1        /* the boundary state (one key/value row)          */
@@ -397,6 +404,171 @@ LS_API int ls_round_paged(ls_state* st, const int32_t* d_draft_ids, const int32_
                           const ls_paged_kv* h_kv, const void* d_verify_hidden, int32_t* d_accept_len,
                           int32_t* d_next_token, const void* d_q, int64_t boundary_k_offset,
                           int64_t boundary_v_offset, float softmax_scale, void* d_out, cudaStream_t stream);
+
+/* ---- block tables and slot maps from request lengths --------------------------------
+ * The paged calls above read a block table and a slot map; these build both on the GPU, so
+ * that a round needs no host step between knowing its lengths and reading its rows. Host
+ * struct, passed by pointer; the pointers in it are DEVICE memory owned by the caller and
+ * are updated in place.
+ *   block_table int32 [b][max_blocks]: entries [0, held[b]) are sequence b's pages.
+ *   held        int32 [b]: pages each sequence holds.
+ *   free_pages  int32 [num_pages]: a stack; entries [0, *free_count) are the free pages.
+ *   free_count  int32 [1].
+ *   page_size   rows per page, any size >= 1.                                           */
+typedef struct {
+  int32_t* block_table;
+  int32_t* held;
+  int32_t* free_pages;
+  int32_t* free_count;
+  int32_t max_blocks;
+  int32_t page_size;
+  int64_t num_pages;
+} ls_page_pool;
+
+/* Gives every sequence the pages for its next rows and writes those rows' slots
+ * (page * page_size + offset; an engine's slot mapping, ls_paged_kv.verify_slots).
+ *   d_len        int64 [b]: rows sequence b holds (its next row is at position len), or
+ *                NULL: the lengths the state itself holds (after its commits).
+ *   d_rows       int32 [b]: new rows of sequence b, 0 .. max_rows, or NULL: max_rows each.
+ *   d_row_begin  NULL: d_slots is [b][max_rows]; entries past a sequence's rows get -1.
+ *                Else int64 [b+1] out: the running sum of the row counts; sequence b's slots
+ *                are d_slots[row_begin[b] .. row_begin[b+1]), and entries past the last
+ *                sequence's rows stay as they were.
+ *   d_slots      int64 [slot_capacity] out; slot_capacity >= b*max_rows where d_row_begin is
+ *                NULL. Packed rows past the capacity are not written (LS_DEVERR_POOL).
+ * Sequence b needs ceil((len + rows) / page_size) pages. The missing ones are taken off the
+ * end of the free list, in the order of the sequences and of their pages: the same result
+ * whatever the launch. From the first sequence on that needs more pages than are left, a
+ * sequence that needs any gets none: it keeps what it held, its rows' slots are -1, and
+ * LS_DEVERR_POOL is set. A row count outside [0, max_rows], a negative length, a held count
+ * outside [0, max_blocks] or rows past max_blocks pages set LS_DEVERR_ROWS, and the sequence
+ * counts as one without new rows. A page id outside [0, num_pages) sets LS_DEVERR_PAGE and
+ * gives slot -1. Uses the state's arrival counts: order this call with the state's other
+ * calls on one stream.                                                                  */
+LS_API int ls_pages_extend(ls_state* st, const ls_page_pool* h_pool, const int64_t* d_len, const int32_t* d_rows,
+                           int32_t max_rows, int64_t* d_row_begin, int64_t* d_slots, int64_t slot_capacity,
+                           cudaStream_t stream);
+
+/* Returns the pages behind every sequence's rows to the free list: after a round whose
+ * drafts were rejected, or with length 0 when a request ends. d_len int64 [b], or NULL: the
+ * state's own lengths. Sequence b keeps ceil(len / page_size) pages; the entries behind
+ * become -1. The pages go to the end of the list in the order that undoes ls_pages_extend:
+ * an extend and a trim to the lengths before it leave the list as it was. A negative length
+ * or a held count outside [0, max_blocks] sets LS_DEVERR_ROWS and the sequence keeps its
+ * pages. When the list would hold more than num_pages, or *free_count is outside
+ * [0, num_pages], LS_DEVERR_POOL is set and nothing changes.                              */
+LS_API int ls_pages_trim(ls_state* st, const ls_page_pool* h_pool, const int64_t* d_len, cudaStream_t stream);
+
+/* ---- a paged KV cache held in 4 bits -------------------------------------------------
+ * A row's D elements are held as D/16 groups: a group's scale is s = e4m3(max|x| / 6), its
+ * 16 codes are e2m1(x / s) (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; nearest, ties to
+ * the even code; 0 where s is 0), and it stands for code * s, which bf16 holds exactly. That
+ * is 4.5 bits an element. A group with an infinite or NaN element gets the scale NaN: all of
+ * it reads as NaN.
+ * Host struct, passed by pointer; the pointers in it are DEVICE memory owned by the caller.
+ *   layers[l]   base of the target's layer l: page p at layers[l] + p * page_stride (bytes;
+ *               16-byte aligned, page_stride a multiple of 16 and >= ls_kv4_page_bytes).
+ *   A page holds, for each KV head in turn, page_size * 9 D / 8 bytes:
+ *               K codes [page_size][D/2], V codes [page_size][D/2], K scales
+ *               [page_size][D/16], V scales [page_size][D/16]; byte i of a row's codes holds
+ *               element 2i in its low half and 2i + 1 in its high half.
+ *   block_table int32 [b][max_blocks], as in ls_paged_kv (only the attention reads it).
+ *   page_size   a power of two, 16 .. 256.
+ * D is 64 or 128 (else LS_ERR_UNSUPPORTED).                                               */
+typedef struct {
+  void* layers[LS_MAX_PAGED_LAYERS];
+  int64_t page_stride;
+  const int32_t* block_table;
+  int32_t max_blocks;
+  int32_t page_size;
+  int64_t num_pages;
+} ls_paged_kv4;
+
+/* Bytes of one page of one layer: n_kv_heads * page_size * 9 D / 8. 0 for an invalid config
+ * or an unsupported page size or head dimension.                                         */
+LS_API size_t ls_kv4_page_bytes(const ls_config* cfg, int32_t page_size);
+
+/* Writes key/value rows into the cache: row i goes to slot d_slots[i] (int64, e.g. from
+ * ls_pages_extend) of layer `layer`.
+ *   d_k, d_v    `dtype`, element (i, g, d) at [i * row_stride + g * D + d]; row_stride >=
+ *               Hkv*D, a multiple of 8 (rows of a packed projection output are read in
+ *               place); 16-byte aligned.
+ * A slot -1 skips its row. Any other slot outside the pool sets LS_DEVERR_PAGE and skips
+ * it. Two rows with the same slot leave a mix of the two there. n_rows >= 0.              */
+LS_API int ls_kv4_append(ls_state* st, const ls_paged_kv4* h_kv, int32_t layer, const void* d_k, const void* d_v,
+                         int64_t row_stride, const int64_t* d_slots, int64_t n_rows, cudaStream_t stream);
+
+/* Reads rows back as `dtype` values (exact in bf16): what the attention over this cache
+ * sees, e.g. as the verify rows of ls_commit_round. Layouts as ls_kv4_append; a row whose
+ * slot is -1 is left as it was, any other slot outside the pool sets LS_DEVERR_PAGE and
+ * leaves it too.                                                                         */
+LS_API int ls_kv4_read_rows(ls_state* st, const ls_paged_kv4* h_kv, int32_t layer, const int64_t* d_slots,
+                            int64_t n_rows, void* d_k, void* d_v, int64_t row_stride, cudaStream_t stream);
+
+/* Workspace bytes that ls_verify_attend_kv4 needs for n_rows query rows per sequence. */
+LS_API size_t ls_verify_workspace_bytes(const ls_config* cfg, int32_t n_rows);
+
+/* The target's attention of a verification pass (Figure 2 (a)) over the 4-bit cache: the
+ * last rows of every sequence against all of its cached rows, causally. n_rows is B + 1 for
+ * a verification pass, 1 for plain decoding.
+ *   d_q         `dtype`, element (b, i, qh, d) at [(b * n_rows + i) * q_stride + qh * D + d];
+ *               q_stride >= Hq*D, a multiple of 8.
+ *   d_rows      int32 [b]: query rows of sequence b (0 .. n_rows), or NULL: n_rows each.
+ *               Output rows i >= rows[b] stay as they were.
+ *   d_kv_len    int64 [b]: cached rows of sequence b, the query rows' own included (they are
+ *               appended before this call): query row i stands at position
+ *               kv_len - rows + i and sees positions 0 .. that one. A row that stands before
+ *               position 0 sees nothing: its output is 0.
+ *   d_out       [b][n_rows][Hq][D]; fp32 with LS_FLAG_OUT_F32, else `dtype`.
+ *   d_workspace >= ls_verify_workspace_bytes bytes of caller scratch, 256-byte aligned; calls
+ *               that may overlap on the GPU (two streams, two graphs) need one each.
+ * n_rows <= B + 1. A kv_len outside [0, max_blocks * page_size] sets LS_DEVERR_PREFIX_LEN and
+ * counts as 0; a row count outside [0, n_rows] sets LS_DEVERR_ROWS and is clamped; a page id
+ * outside [0, num_pages) sets LS_DEVERR_PAGE and is read as page 0. What lies in the cache
+ * behind kv_len (stale rows, NaN scales) does not reach the output. bf16 states run on the
+ * tensor cores: keys and values are exact there, queries and softmax weights are rounded to
+ * fp16 (11 bits; queries after scaling each row to a largest element near 1); fp32 states
+ * run in fp32 on CUDA cores. Repeated calls give the same bits.                           */
+LS_API int ls_verify_attend_kv4(const ls_state* st, const ls_paged_kv4* h_kv, int32_t layer, const void* d_q,
+                                int64_t q_stride, int32_t n_rows, const int32_t* d_rows, const int64_t* d_kv_len,
+                                float softmax_scale, void* d_out, void* d_workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/* ---- the projections with each request's own low-rank adapter ------------------------
+ * Host struct, passed by pointer; the pointers in it are DEVICE memory owned by the caller,
+ * 16-byte aligned.
+ *   a_q, a_kv   bf16 [n_adapters][L][rank][hidden]
+ *   b_q         bf16 [n_adapters][L][Hq D][rank];  b_kv  bf16 [n_adapters][L][2 Hkv D][rank]
+ *   scale       fp32 [n_adapters]
+ *   adapter_of  int32 [b]: the adapter of sequence b, or -1 for none.
+ *   rank        a multiple of 8, 8 .. 128 (pad smaller ones with zero rows and columns).   */
+typedef struct {
+  const void* a_q;
+  const void* b_q;
+  const void* a_kv;
+  const void* b_kv;
+  const float* scale;
+  const int32_t* adapter_of;
+  int32_t n_adapters;
+  int32_t rank;
+} ls_lora;
+
+/* Workspace bytes of ls_draft_prologue_lora. 0 for an invalid config or rank. */
+LS_API size_t ls_lora_workspace_bytes(const ls_config* cfg, int32_t rank);
+
+/* ls_draft_prologue with sequence b's adapter a = adapter_of[b] added to both projections:
+ *   q[b][l][i]  = W_q[l]  x[b][l][i]      + scale[a] B_q[a][l]  (A_q[a][l]  x[b][l][i])
+ *   bkv[b][l]   = W_kv[l] boundary[b][l]  + scale[a] B_kv[a][l] (A_kv[a][l] boundary[b][l])
+ * summed in fp32 and rounded to bf16 once. The sum over the rank is taken apart from the one
+ * over the hidden size; a sequence without an adapter gets what ls_draft_prologue gives it,
+ * and nothing of one sequence's adapter reaches another's rows. An id outside
+ * [-1, n_adapters) sets LS_DEVERR_ADAPTER and counts as -1. Arguments, limits and launch
+ * rules as ls_draft_prologue; the adapters' weights and adapter_of may be written by the
+ * kernel launched just before. d_workspace: >= ls_lora_workspace_bytes bytes, 256-byte
+ * aligned; calls that may overlap on the GPU need one each.                               */
+LS_API int ls_draft_prologue_lora(const ls_state* st, const void* d_w_kv, const void* d_w_q, const void* d_x,
+                                  const ls_lora* h_lora, void* d_bkv, void* d_q, void* d_workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
 
 /* One whole decoding round: ls_commit_round, then ls_draft_attend over all layers, for
  * drafters whose boundary keys/values are slices of the new boundary hidden vector:

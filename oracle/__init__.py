@@ -9,3 +9,6 @@ from .longspark_oracle import (  # noqa: F401
     attention_slots, commit_round, commit_round_paged, draft_attend, draft_prologue, empty_views, paged_rows, prefill, prefill_paged, retain_row, segment_count,
     softmax_scale_for, state_bytes, to_f64, view_of_slots, views_from_scratch,
 )
+from .serving_oracle import (  # noqa: F401
+    attend_rows, kv4_decode, kv4_encode, kv4_row, kv4_sections, pages_extend, pages_trim, project_lora,
+)
