@@ -9,6 +9,8 @@
 
 namespace ls {
 
+cudaError_t launch_verify_mma(const VerArgs& a, cudaStream_t stream);
+
 namespace {
 
 constexpr int kVThreads = 128;
@@ -26,6 +28,8 @@ __global__ void __launch_bounds__(kVThreads) verify_simt_kernel(const VerArgs a)
   __shared__ float ref_s[kSimtRows], sum_s[kSimtRows], alpha_s[kSimtRows];
   __shared__ int nan_s[D / kKv4Group];  // first chunk-relative position, from c0 on, of a NaN value group
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dependency_wait();
+  allow_dependent_launch();
   VerCursor cur = ver_begin(a, blockIdx.x);
   VerPiece p;
   while (ver_next(a, cur, p)) {
@@ -240,15 +244,22 @@ __global__ void __launch_bounds__(kVThreads) verify_join_kernel(const VerArgs a)
   }
 }
 
+enum VerKernel { kVerSimt, kVerMma };
 struct VerShape {
+  VerKernel kernel;
   int MR, ctas;  // rows per tile, CTAs per SM
 };
-VerShape ver_shape(int, int, int) { return {kSimtRows, kSimtCtas}; }
+VerShape ver_shape(const ls_config& c, int n_rows) {
+  const int M = n_rows * (c.n_q_heads / c.n_kv_heads);
+  if (c.dtype == LS_BF16 && !(c.flags & LS_FLAG_FORCE_SIMT) && M <= kMmaMostRows)
+    return {kVerMma, (M + 7) / 8 * 8, mma_ctas(M)};
+  return {kVerSimt, kSimtRows, kSimtCtas};
+}
 
 }  // namespace
 
 size_t verify_workspace_bytes(const ls_config& c, int n_rows) {
-  const VerShape v = ver_shape(c.dtype, c.flags, n_rows * (c.n_q_heads / c.n_kv_heads));
+  const VerShape v = ver_shape(c, n_rows);
   return size_t(2) * kVerMaxSms * v.ctas * v.MR * (size_t(c.head_dim) + 2) * 4;
 }
 
@@ -256,7 +267,7 @@ cudaError_t launch_verify(const Dev& p, const ls_config& c, const ls_paged_kv4& 
                           int64_t q_stride, int n_rows, const int32_t* rows, const int64_t* kv_len, float scale,
                           void* out, void* ws, int sms, cudaStream_t stream) {
   const int grp = p.Hq / p.Hkv;
-  const VerShape v = ver_shape(c.dtype, c.flags, n_rows * grp);
+  const VerShape v = ver_shape(c, n_rows);
   VerArgs a{};
   a.base = static_cast<const unsigned char*>(kv.layers[layer]);
   a.page_stride = kv.page_stride;
@@ -287,18 +298,19 @@ cudaError_t launch_verify(const Dev& p, const ls_config& c, const ls_paged_kv4& 
   a.part_o = static_cast<float*>(ws);
   a.part_ml = a.part_o + int64_t(2) * a.G * v.MR * p.D;
   if (int64_t(p.b) * a.HM > INT32_MAX) return cudaErrorNotSupported;
-  if (p.dtype == LS_F32) {
-    if (p.D == 128) verify_simt_kernel<float, 128><<<a.G, kVThreads, 0, stream>>>(a);
-    else verify_simt_kernel<float, 64><<<a.G, kVThreads, 0, stream>>>(a);
+  cudaError_t e;
+  if (v.kernel == kVerMma) {
+    e = launch_verify_mma(a, stream);
+  } else if (p.dtype == LS_F32) {
+    e = p.D == 128 ? ver_launch(verify_simt_kernel<float, 128>, a.G, kVThreads, 0, stream, a)
+                   : ver_launch(verify_simt_kernel<float, 64>, a.G, kVThreads, 0, stream, a);
   } else {
-    if (p.D == 128) verify_simt_kernel<__nv_bfloat16, 128><<<a.G, kVThreads, 0, stream>>>(a);
-    else verify_simt_kernel<__nv_bfloat16, 64><<<a.G, kVThreads, 0, stream>>>(a);
+    e = p.D == 128 ? ver_launch(verify_simt_kernel<__nv_bfloat16, 128>, a.G, kVThreads, 0, stream, a)
+                   : ver_launch(verify_simt_kernel<__nv_bfloat16, 64>, a.G, kVThreads, 0, stream, a);
   }
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (p.D == 128) verify_join_kernel<128><<<p.b * a.HM, kVThreads, 0, stream>>>(a);
-  else verify_join_kernel<64><<<p.b * a.HM, kVThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return p.D == 128 ? ver_launch(verify_join_kernel<128>, p.b * a.HM, kVThreads, 0, stream, a)
+                    : ver_launch(verify_join_kernel<64>, p.b * a.HM, kVThreads, 0, stream, a);
 }
 
 }  // namespace ls

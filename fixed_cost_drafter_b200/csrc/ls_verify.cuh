@@ -15,6 +15,9 @@ namespace ls {
 
 constexpr int kVerChunk = 128;   // keys per chunk
 constexpr int kVerMaxSms = 160;  // CTA slots are sized for at most this many SMs
+constexpr int kMmaMostRows = 24;  // query rows per KV head up to which the warp-level kernel runs
+// its CTAs per SM: registers hold 3 with up to 8 rows (shared memory as well), then 2 and 1
+__host__ __device__ constexpr int mma_ctas(int rows) { return rows <= 8 ? 3 : (rows <= 16 ? 2 : 1); }
 constexpr int kSimtRows = 8;     // MR of the CUDA-core kernel
 constexpr int kSimtCtas = 4;     // its CTAs per SM
 
@@ -177,6 +180,23 @@ __device__ inline void ver_store(const VerArgs& a, int64_t at, const float* v) {
 // Where row i, query head h of sequence b starts in the output.
 __device__ inline int64_t ver_out_at(const VerArgs& a, int b, int i, int h) {
   return ((int64_t(b) * a.n_rows + i) * a.Hq + h) * a.D;
+}
+
+// A launch that may start while the kernel before it on the stream still runs: the kernels here
+// wait for it (grid_dependency_wait) before they read or write anything.
+template <typename... A>
+inline cudaError_t ver_launch(void (*kernel)(A...), int grid, int threads, int smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace ls
