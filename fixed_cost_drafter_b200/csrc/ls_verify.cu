@@ -10,6 +10,7 @@
 namespace ls {
 
 cudaError_t launch_verify_mma(const VerArgs& a, cudaStream_t stream);
+cudaError_t launch_verify_tc(const VerArgs& a, cudaStream_t stream);
 
 namespace {
 
@@ -244,15 +245,17 @@ __global__ void __launch_bounds__(kVThreads) verify_join_kernel(const VerArgs a)
   }
 }
 
-enum VerKernel { kVerSimt, kVerMma };
+enum VerKernel { kVerSimt, kVerMma, kVerTc };
 struct VerShape {
   VerKernel kernel;
   int MR, ctas;  // rows per tile, CTAs per SM
 };
 VerShape ver_shape(const ls_config& c, int n_rows) {
   const int M = n_rows * (c.n_q_heads / c.n_kv_heads);
-  if (c.dtype == LS_BF16 && !(c.flags & LS_FLAG_FORCE_SIMT) && M <= kMmaMostRows)
-    return {kVerMma, (M + 7) / 8 * 8, mma_ctas(M)};
+  if (c.dtype == LS_BF16 && !(c.flags & LS_FLAG_FORCE_SIMT)) {
+    if (M <= kMmaMostRows) return {kVerMma, (M + 7) / 8 * 8, mma_ctas(M)};
+    if (M <= kTcRows) return {kVerTc, kTcRows, 1};
+  }
   return {kVerSimt, kSimtRows, kSimtCtas};
 }
 
@@ -301,6 +304,8 @@ cudaError_t launch_verify(const Dev& p, const ls_config& c, const ls_paged_kv4& 
   cudaError_t e;
   if (v.kernel == kVerMma) {
     e = launch_verify_mma(a, stream);
+  } else if (v.kernel == kVerTc) {
+    e = launch_verify_tc(a, stream);
   } else if (p.dtype == LS_F32) {
     e = p.D == 128 ? ver_launch(verify_simt_kernel<float, 128>, a.G, kVThreads, 0, stream, a)
                    : ver_launch(verify_simt_kernel<float, 64>, a.G, kVThreads, 0, stream, a);

@@ -18,6 +18,7 @@ constexpr int kVerMaxSms = 160;  // CTA slots are sized for at most this many SM
 constexpr int kMmaMostRows = 24;  // query rows per KV head up to which the warp-level kernel runs
 // its CTAs per SM: registers hold 3 with up to 8 rows (shared memory as well), then 2 and 1
 __host__ __device__ constexpr int mma_ctas(int rows) { return rows <= 8 ? 3 : (rows <= 16 ? 2 : 1); }
+constexpr int kTcRows = 128;      // MR of the tcgen05 kernel: a state's query rows per KV head are at most 128
 constexpr int kSimtRows = 8;     // MR of the CUDA-core kernel
 constexpr int kSimtCtas = 4;     // its CTAs per SM
 

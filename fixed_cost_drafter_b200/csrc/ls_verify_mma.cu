@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kMWarps = 4;                      // consumer warps
 constexpr int kMThreads = (kMWarps + 1) * 32;   // and a producer warp
-constexpr int kMStages = 4;
+constexpr int kMStages = 3;
 constexpr float kMRoom = 8.f;    // log2 of the largest weight when the reference moves
 constexpr float kMMost = 15.f;   // and the log2 at which it has to
 
