@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(kVThreads) verify_simt_kernel(const VerArgs a)
 }
 
 // Joins the pieces of cut tiles, zeroes the rows of empty sequences and flags arguments
-// outside their range. One CTA per tile, a warp per row.
+// outside their range. A warp per row (one CTA per tile and four rows): its lanes take the
+// pieces' references and sums, then D / 32 output elements each, piece by piece in range order.
 template <int D>
 __global__ void __launch_bounds__(kVThreads) verify_join_kernel(const VerArgs a) {
   constexpr int kPer = D / 32;  // output elements per lane
@@ -200,49 +201,59 @@ __global__ void __launch_bounds__(kVThreads) verify_join_kernel(const VerArgs a)
   const int g = hm / mts, m0 = (hm - g * mts) * a.MR;
   const int64_t n = ver_chunks(a, b);
   const int rows = ver_rows(a, b);
-  if (hm == 0 && threadIdx.x == 0) {
+  if (hm == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
     if (a.kv_len[b] != ver_len(a, b)) set_err(a.err, LS_DEVERR_PREFIX_LEN);
     if (a.rows && a.rows[b] != rows) set_err(a.err, LS_DEVERR_ROWS);
   }
-  const int64_t before = ver_chunks_before(a, b), T = ver_chunks_before(a, a.b) * a.HM;
-  const int64_t G = T < a.G ? T : a.G;
-  const int64_t t0 = before * a.HM + hm * n, t1 = t0 + n;
-  grid_dependency_wait();
-  int c_first = 0, c_last = 0;
+  const int r = int(blockIdx.y) * (kVThreads / 32) + warp;
+  const int i = (m0 + r) / a.grp, j = (m0 + r) - i * a.grp;
+  if (r >= a.MR || m0 + r >= a.M || i >= rows) return;
+  int c_first = 0, c_last = -1;
   if (n > 0) {  // the CTAs whose ranges hold the tile's first and last chunk
+    const int64_t T = ver_chunks_before(a, a.b) * a.HM, t0 = ver_chunks_before(a, b) * a.HM + hm * n;
+    const int64_t G = T < a.G ? T : a.G;
     c_first = int(((t0 + 1) * G + T - 1) / T) - 1;
-    c_last = int((t1 * G + T - 1) / T) - 1;
+    c_last = int(((t0 + n) * G + T - 1) / T) - 1;
     if (c_first == c_last) return;  // the tile's CTA has written it
   }
-  for (int r = warp; r < a.MR && m0 + r < a.M; r += kVThreads / 32) {
-    const int i = (m0 + r) / a.grp, j = (m0 + r) - i * a.grp;
-    if (i >= rows) break;
-    float o[kPer];
+  // the first piece starts its tile (an odd slot), the others start their CTAs' ranges
+  auto at = [&](int c) { return (int64_t(2 * c) + (c == c_first ? 1 : 0)) * a.MR + r; };
+  grid_dependency_wait();
+  float o[kPer];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-    if (n > 0) {
-      auto slot_of = [&](int c) { return 2 * c + (c * T / G <= t0 ? 1 : 0); };
-      float top = -INFINITY;
-      for (int c = c_first + lane; c <= c_last; c += 32)
-        top = fmaxf(top, a.part_ml[(int64_t(slot_of(c)) * a.MR + r) * 2]);
+  for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+  float top = -INFINITY;
+  for (int c = c_first + lane; c <= c_last; c += 32) top = fmaxf(top, a.part_ml[at(c) * 2]);
 #pragma unroll
-      for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-      const float mu = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-      for (int c = c_first; c <= c_last; ++c) {
-        const int64_t at = int64_t(slot_of(c)) * a.MR + r;
-        const float w = exp2f(a.part_ml[at * 2] - mu);
-        sum = fmaf(w, a.part_ml[at * 2 + 1], sum);
-        const float* src = a.part_o + at * D + lane * kPer;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] = fmaf(w, src[e], o[e]);
-      }
-      const float inv = sum != 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] *= inv;
+  for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+  const float mu = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  for (int c0 = c_first; c0 <= c_last; c0 += 32) {
+    float w = 0.f;
+    if (c0 + lane <= c_last) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at(c0 + lane) * 2);
+      w = exp2f(ml.x - mu);
+      sum = fmaf(w, ml.y, sum);
     }
-    ver_store<kPer>(a, ver_out_at(a, b, i, g * a.grp + j) + lane * kPer, o);
+    const int cn = min(32, c_last - c0 + 1);
+#pragma unroll 8
+    for (int u = 0; u < cn; ++u) {
+      const float wu = __shfl_sync(0xffffffffu, w, u);
+      const float* src = a.part_o + at(c0 + u) * D + lane * kPer;
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(src + e);
+        o[e] = fmaf(wu, x.x, o[e]);
+        o[e + 1] = fmaf(wu, x.y, o[e + 1]);
+      }
+    }
   }
+#pragma unroll
+  for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) o[e] *= inv;
+  ver_store<kPer>(a, ver_out_at(a, b, i, g * a.grp + j) + lane * kPer, o);
 }
 
 enum VerKernel { kVerSimt, kVerMma, kVerTc };
@@ -314,8 +325,9 @@ cudaError_t launch_verify(const Dev& p, const ls_config& c, const ls_paged_kv4& 
                    : ver_launch(verify_simt_kernel<__nv_bfloat16, 64>, a.G, kVThreads, 0, stream, a);
   }
   if (e != cudaSuccess) return e;
-  return p.D == 128 ? ver_launch(verify_join_kernel<128>, p.b * a.HM, kVThreads, 0, stream, a)
-                    : ver_launch(verify_join_kernel<64>, p.b * a.HM, kVThreads, 0, stream, a);
+  const dim3 grid(p.b * a.HM, ((a.M < v.MR ? a.M : v.MR) + kVThreads / 32 - 1) / (kVThreads / 32));
+  return p.D == 128 ? ver_launch(verify_join_kernel<128>, grid, kVThreads, 0, stream, a)
+                    : ver_launch(verify_join_kernel<64>, grid, kVThreads, 0, stream, a);
 }
 
 }  // namespace ls

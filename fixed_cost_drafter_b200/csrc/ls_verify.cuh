@@ -186,9 +186,9 @@ __device__ inline int64_t ver_out_at(const VerArgs& a, int b, int i, int h) {
 // A launch that may start while the kernel before it on the stream still runs: the kernels here
 // wait for it (grid_dependency_wait) before they read or write anything.
 template <typename... A>
-inline cudaError_t ver_launch(void (*kernel)(A...), int grid, int threads, int smem, cudaStream_t stream, A... args) {
+inline cudaError_t ver_launch(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

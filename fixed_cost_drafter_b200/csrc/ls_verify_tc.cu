@@ -5,8 +5,8 @@
 // about as long as the bytes of the cache take to arrive, and the operands have to be made
 // first: shared memory carries every fp16 operand twice (written by the conversion, read by
 // the MMA). So nothing else goes through shared memory: codes come from global memory straight
-// into the converting threads' registers (one chunk ahead, behind an L2 prefetch four chunks
-// ahead), Q and the weights P are the MMAs' A operands in TMEM.
+// into the converting threads' registers, two chunks ahead, and Q and the weights P are the
+// MMAs' A operands in TMEM.
 //
 // One CTA per SM, 14 warps; the roles meet at mbarriers:
 //   warps 4-11  conversion: warp w takes 16 rows of each 128-key chunk, a thread 16 codes (one
@@ -14,12 +14,14 @@
 //               each. A group's two 16-byte pieces go to different 64-column halves (D = 128),
 //               so that eight threads fill a whole 128-byte row; Q and the output columns
 //               follow the same order.
-//   warp 12     S = Q K^T, 64 keys at a time into one of four 64-column buffers
-//   warps 0-3   softmax, a thread per query row: weights 2^(x - r) in fp16, written over S. The
-//               reference r only moves when 64 weights sum to more than 2^15 (fp16 holds up to
-//               65504); it is then the maximum less 8, as in ls_verify_mma.cu, and the row of
-//               O is scaled in TMEM. The sum is needed anyway: the check costs no maximum.
-//   warp 13     O += P V
+//   warp 12     S = Q K^T of a chunk into one of two 128-column buffers (8 MMAs of N = 128: an
+//               MMA costs its issuing thread about 80 cycles whatever its N)
+//   warps 0-3   softmax, a thread per query row, 64 keys at a time: weights 2^(x - r) in fp16,
+//               written over S. The reference r only moves when 64 weights sum to more than
+//               2^15 (fp16 holds up to 65504); it is then the maximum less 8, as in
+//               ls_verify_mma.cu, and the row of O is scaled in TMEM. The sum is needed anyway:
+//               the check costs no maximum.
+//   warp 13     O += P V, 64 keys at a time
 // TMEM columns: S / P 0-255, O 256-383, Q 384-447.
 // Rounding, exactness of the held values and NaN groups: as in ls_verify_mma.cu.
 #include "ls_verify.cuh"
@@ -31,17 +33,16 @@ namespace {
 
 constexpr int kTThreads = 448;
 constexpr int kTConv = 8;          // conversion warps
-constexpr int kTSub = 64;          // keys per S buffer
-constexpr int kTBufs = 4;          // S / P buffers
+constexpr int kTSub = 64;          // keys the softmax takes at a time
 constexpr uint32_t kTCols = 512, kTO = 256, kTQ = 384;
 constexpr float kTRoom = 8.f;
 constexpr float kTMostSum = 32768.f;
-constexpr int kTAhead = 4;         // chunks between the L2 prefetch and the use
 constexpr int kNanSlots = 4;       // pieces whose NaN positions are kept (conversion runs at most 2 ahead)
 
 struct TBars {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-  uint64_t s_full[kTBufs], p_full[kTBufs], p_free[kTBufs];
+  uint64_t s_full[2], p_full[4], p_free[2];  // p_full: [buffer][half]
+  uint64_t h_done;  // the first half's P V
   uint64_t q_full, o_full, o_free, drain[2];
   uint32_t tmem_base, abort;
   int nan_at[kNanSlots][8];
@@ -64,6 +65,12 @@ __device__ inline bool twait_warp(TBars& s, uint64_t* bar, uint32_t parity, int3
 // kind::f16 with fp16 A/B, fp32 D
 constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
   return (1u << 4) | (uint32_t(b_mn_major) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+}
+
+__device__ inline bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 __device__ inline void tmem_ld64(uint32_t taddr, float (&v)[64]) {
@@ -114,27 +121,6 @@ __device__ inline uint32_t pack_half2(float lo, float hi) {
   return r;
 }
 
-// The line of chunks of a CTA, one at a time across pieces.
-struct TLine {
-  VerCursor cur;
-  VerPiece p;
-  int64_t c;
-  int piece;
-  bool live;
-};
-__device__ inline void line_begin(const VerArgs& a, TLine& l) {
-  l.cur = ver_begin(a, blockIdx.x);
-  l.piece = 0;
-  l.live = ver_next(a, l.cur, l.p);
-  l.c = l.p.c0;
-}
-__device__ inline void line_step(const VerArgs& a, TLine& l) {
-  if (++l.c < l.p.c1) return;
-  ++l.piece;
-  l.live = ver_next(a, l.cur, l.p);
-  if (l.live) l.c = l.p.c0;
-}
-
 // Column position n of the K / V tiles holds dim dim_of(n): see the conversion.
 template <int D>
 __device__ constexpr int dim_of(int n) {
@@ -161,13 +147,15 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
       mbar_init(&s.vempty[i], 1);
       mbar_init(&s.drain[i], 1);
     }
-    for (int i = 0; i < kTBufs; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], 32 * act);
+      mbar_init(&s.p_full[2 * i], 32 * act);
+      mbar_init(&s.p_full[2 * i + 1], 32 * act);
       mbar_init(&s.p_free[i], 1);
     }
     mbar_init(&s.q_full, 32 * act);
     mbar_init(&s.o_full, 1);
+    mbar_init(&s.h_done, 1);
     mbar_init(&s.o_free, 32 * act);
     s.abort = 0;
     for (int i = 0; i < kNanSlots * 8; ++i) s.nan_at[i >> 3][i & 7] = kVerNone;
@@ -190,187 +178,207 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
     // ---------------------------------------------------------------- conversion
     const int cw = warp - 4, row0 = cw * 16;
     const int r = lane / kGroups, g = lane % kGroups;  // this thread's row (of kRowStep) and group
-    TLine look, line;
-    line_begin(a, look);
-    line = look;
-    // where this warp's 16 rows of the next chunks lie: codes of the keys, and from there the
-    // distance to their scales; null: no row of them is held
-    const unsigned char* at[kTAhead];
-    int to_scales[kTAhead];
-    int32_t entry = 0;
-    auto load_entry = [&]() {
-      const int64_t pos = look.c * kVerChunk + row0;
-      entry = look.live && pos < look.p.len ? __ldg(a.table + int64_t(look.p.b) * a.max_blocks + (pos >> a.page_shift)) : 0;
-    };
     const int ps = a.page_size;
-    auto resolve = [&](const unsigned char*& ptr, int& dist) {  // of the chunk `look` stands at
-      const int64_t pos = look.c * kVerChunk + row0;
-      ptr = nullptr;
-      dist = 0;
-      if (!look.live) return;
-      if (pos < look.p.len) {
-        int64_t page = entry;
-        if (page < 0 || page >= a.num_pages) {
-          set_err(a.err, LS_DEVERR_PAGE);
-          page = 0;
-        }
-        const int off = int(pos & (ps - 1));
-        ptr = a.base + page * a.page_stride + int64_t(look.p.hm) * kv4_block_bytes(ps, D) + off * (D / 2);
-        dist = ps * D + off * (D / kKv4Group) - off * (D / 2);
-        if (lane < 4) {  // lanes 0, 1: codes of K, V; 2, 3: scales
-          const unsigned char* from = lane < 2 ? ptr + lane * ps * (D / 2) : ptr + dist + (lane - 2) * ps * (D / kKv4Group);
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(lane < 2 ? 16 * (D / 2) : 16 * (D / kKv4Group))
-                       : "memory");
-        }
+    VerCursor cur = ver_begin(a, blockIdx.x);
+    const int total = int(cur.left);  // chunks of this CTA
+    // The lookup walks ahead of the conversion: the page of a chunk is looked up three chunks
+    // ahead, its codes are loaded two ahead.
+    VerPiece p;
+    int64_t pos = 0;   // of this warp's 16 rows in the chunk looked up next
+    int left = 0, piece = -1, rel = 0;
+    int32_t entry = 0;
+    auto look_up = [&]() {
+      if (left == 0) {
+        if (!ver_next(a, cur, p)) return;
+        left = int(p.c1 - p.c0);
+        pos = p.c0 * kVerChunk + row0;
+        rel = row0;
+        ++piece;
       }
-      line_step(a, look);
+      entry = pos < p.len ? __ldg(a.table + int64_t(p.b) * a.max_blocks + (pos >> a.page_shift)) : 0;
     };
-    load_entry();
-#pragma unroll
-    for (int i = 0; i < kTAhead; ++i) {
-      resolve(at[i], to_scales[i]);
-      load_entry();
-    }
-    uint2 kc[kIter], vc[kIter];
-    uint32_t ks[kIter], vs[kIter];
+    struct Rows {  // a chunk's 16 rows of this warp: codes and scales in flight
+      uint2 w[2][kIter];
+      uint32_t sc[2][kIter];
+      int held, rel, piece;  // rows below the sequence's length, position in the piece, piece
+    };
+    Rows rows[2];
+    const unsigned char* src = nullptr;  // the chunk whose rows are loaded next: its keys' codes
+    int to_scales = 0;
     const int code_at = r * (D / 2) + g * 8, scale_at = r * kGroups + g;
-    auto load_rows = [&](const unsigned char* p, const unsigned char* sp, uint2 (&w)[kIter], uint32_t (&sc)[kIter]) {
+    // the chunk looked up becomes the next to load, and the one behind it is looked up
+    auto resolve = [&](Rows& q) {
+      src = nullptr;
+      q.held = 0;
+      if (left > 0) {
+        if (pos < p.len) {
+          int64_t page = entry;
+          if (page < 0 || page >= a.num_pages) {
+            set_err(a.err, LS_DEVERR_PAGE);
+            page = 0;
+          }
+          const int off = int(pos) & (ps - 1);
+          src = a.base + page * a.page_stride + int64_t(p.hm) * kv4_block_bytes(ps, D) + off * (D / 2);
+          to_scales = ps * D + off * (D / kKv4Group) - off * (D / 2);
+          q.held = p.len - pos < 16 ? int(p.len - pos) : 16;
+        }
+        q.rel = rel;
+        q.piece = piece & (kNanSlots - 1);
+        pos += kVerChunk;
+        rel += kVerChunk;
+        --left;
+      }
+      look_up();
+    };
+    auto load = [&](Rows& q, int v) {
+      const unsigned char* c = src + v * ps * (D / 2) + code_at;
+      const unsigned char* sp = src + to_scales + v * ps * (D / kKv4Group) + scale_at;
 #pragma unroll
       for (int i = 0; i < kIter; ++i) {
-        w[i] = make_uint2(0u, 0u);
-        sc[i] = 0u;
-        if (p) {
+        q.w[v][i] = make_uint2(0u, 0u);
+        q.sc[v][i] = 0u;
+        if (src) {
           asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                       : "=r"(w[i].x), "=r"(w[i].y)
-                       : "l"(p + code_at + i * kRowStep * (D / 2)));
-          asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(sc[i]) : "l"(sp + scale_at + i * kRowStep * kGroups));
+                       : "=r"(q.w[v][i].x), "=r"(q.w[v][i].y)
+                       : "l"(c + i * kRowStep * (D / 2)));
+          asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(q.sc[v][i]) : "l"(sp + i * kRowStep * kGroups));
         }
       }
     };
-    auto load_k = [&]() { load_rows(at[0], at[0] + to_scales[0], kc, ks); };
-    auto load_v = [&]() {
-      load_rows(at[0] ? at[0] + ps * (D / 2) : nullptr, at[0] + to_scales[0] + ps * (D / kKv4Group), vc, vs);
-    };
-    // the thread's 16 codes of row `row` as two 16-byte pieces of the tile
-    auto put = [&](unsigned char* tile, int row, const uint2& w, uint32_t scale) {
+    // the thread's 16 codes of a row as two 16-byte pieces of the tile
+    auto put = [&](unsigned char* line0, const uint2& w, uint32_t scale) {
       const uint32_t s2 = e4m3x2_to_half2(uint16_t(scale * 0x101u));
       uint32_t h[8];
       e2m1x8_to_half2(w.x, h);
       e2m1x8_to_half2(w.y, h + 4);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[j] = hmul2(h[j], s2);
-      unsigned char* line0 = tile + row * 128;
-      const int x = row & 7;
-      if constexpr (D == 128) {
-        *reinterpret_cast<uint4*>(line0 + ((g ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(line0 + kHalf + ((g ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-      } else {
-        *reinterpret_cast<uint4*>(line0 + (((2 * g) ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(line0 + (((2 * g + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-      }
+      *reinterpret_cast<uint4*>(line0) = make_uint4(h[0], h[1], h[2], h[3]);
+      // (D = 64: pieces 2 g and 2 g + 1 of the row, whose places differ in the lowest bit)
+      unsigned char* second = D == 128 ? line0 + kHalf
+                                       : reinterpret_cast<unsigned char*>(reinterpret_cast<uintptr_t>(line0) ^ 16);
+      *reinterpret_cast<uint4*>(second) = make_uint4(h[4], h[5], h[6], h[7]);
     };
-    load_k();
-    load_v();
-    for (int k = 0; line.live; ++k) {
-      const int st = k & 1;
-      // the chunk after this one moves up; one more is looked up behind the others
+    // the first piece's place in the thread's rows: row0 + r + i kRowStep; 8 rows apart the
+    // swizzle repeats
+    int place[kIter];
 #pragma unroll
-      for (int i = 0; i + 1 < kTAhead; ++i) {
-        at[i] = at[i + 1];
-        to_scales[i] = to_scales[i + 1];
-      }
-      resolve(at[kTAhead - 1], to_scales[kTAhead - 1]);
-      load_entry();
-      if (k >= 2 && !twait_warp(s, &s.kempty[st], uint32_t((k >> 1) - 1) & 1, a.err)) break;
+    for (int i = 0; i < kIter; ++i) {
+      const int row = row0 + r + i * kRowStep;
+      place[i] = row * 128 + (((D == 128 ? g : 2 * g) ^ (row & 7)) << 4);
+    }
+    look_up();
 #pragma unroll
-      for (int i = 0; i < kIter; ++i) put(kbuf + st * kTile, row0 + r + i * kRowStep, kc[i], ks[i]);
-      load_k();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.kfull[st]);
-      bool nan = false;
+    for (int i = 0; i < 2; ++i) {
+      resolve(rows[i]);
+      load(rows[i], 0);
+      load(rows[i], 1);
+    }
+    bool ok = true;
+    for (int k0 = 0; k0 < total && ok; k0 += 2) {
 #pragma unroll
-      for (int i = 0; i < kIter; ++i) nan |= nan_scale(vs[i]);
-      if (nan) {  // such a group takes part as zeros (ls_verify.cuh)
+      for (int st = 0; st < 2; ++st) {
+        const int k = k0 + st;
+        if (k >= total) break;
+        Rows& q = rows[st];
+        const int held = q.held, at = q.rel, slot = q.piece;
+        resolve(q);  // chunk k + 2
+        if (k >= 2 && !twait_warp(s, &s.kempty[st], uint32_t((k >> 1) - 1) & 1, a.err)) { ok = false; break; }
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          if (!nan_scale(vs[i])) continue;
-          const int64_t pos = line.c * kVerChunk + row0 + r + i * kRowStep;
-          if (pos < line.p.len) atomicMin(&s.nan_at[line.piece & (kNanSlots - 1)][g], int(pos - line.p.c0 * kVerChunk));
-          vs[i] = 0u;
+        for (int i = 0; i < kIter; ++i) put(kbuf + st * kTile + place[i], q.w[0][i], q.sc[0][i]);
+        load(q, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.kfull[st]);
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) nan |= nan_scale(q.sc[1][i]);
+        if (nan) {  // such a group takes part as zeros (ls_verify.cuh)
+#pragma unroll
+          for (int i = 0; i < kIter; ++i) {
+            if (!nan_scale(q.sc[1][i])) continue;
+            if (r + i * kRowStep < held) atomicMin(&s.nan_at[slot][g], at + r + i * kRowStep);
+            q.sc[1][i] = 0u;
+          }
         }
-      }
-      if (k >= 2 && !twait_warp(s, &s.vempty[st], uint32_t((k >> 1) - 1) & 1, a.err)) break;
+        if (k >= 2 && !twait_warp(s, &s.vempty[st], uint32_t((k >> 1) - 1) & 1, a.err)) { ok = false; break; }
 #pragma unroll
-      for (int i = 0; i < kIter; ++i) put(vbuf + st * kTile, row0 + r + i * kRowStep, vc[i], vs[i]);
-      load_v();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.vfull[st]);
-      line_step(a, line);
+        for (int i = 0; i < kIter; ++i) put(vbuf + st * kTile + place[i], q.w[1][i], q.sc[1][i]);
+        load(q, 1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.vfull[st]);
+      }
     }
   } else if (warp == 12 || warp == 13) {
     // ---------------------------------------------------------------- MMA issuers
-    TLine line;
-    line_begin(a, line);
-    if (lane == 0) {
-      const bool qk = warp == 12;
-      const uint64_t desc0 = qk ? sdesc(smem_u32(kbuf), 16, 1024) : sdesc(smem_u32(vbuf), kHalf, 1024);
-      int sub = 0;  // sub-chunks so far
-      bool ok = true;
-      for (int k = 0; line.live && ok; ++k) {
+    // the whole warp walks the chunks; one elected lane issues
+    const bool qk = warp == 12;
+    VerCursor cur = ver_begin(a, blockIdx.x);
+    VerPiece p;
+    const uint64_t desc0 = qk ? sdesc(smem_u32(kbuf), 16, 1024) : sdesc(smem_u32(vbuf), kHalf, 1024);
+    bool ok = true;
+    int k = 0;
+    for (int piece = 0; ok && ver_next(a, cur, p); ++piece) {
+      const int n = int(p.c1 - p.c0);
+      if (qk) {
+        ok = twait_warp(s, &s.q_full, uint32_t(piece) & 1, a.err);
+      } else if (piece > 0) {
+        ok = twait_warp(s, &s.o_free, uint32_t(piece - 1) & 1, a.err);
+        // the output of the piece before is out: its NaN positions make room for another's
+        if (lane < 8) s.nan_at[(piece - 1) & (kNanSlots - 1)][lane] = kVerNone;
+        __syncwarp();
+      }
+      for (int c = 0; c < n && ok; ++c, ++k) {
         const int st = k & 1;
-        const bool first = line.c == line.p.c0, last = line.c == line.p.c1 - 1;
-        const int subs = line.p.len - line.c * kVerChunk > kTSub ? 2 : 1;
-        if (first) {
-          if (qk) ok = twait(s, &s.q_full, uint32_t(line.piece) & 1, a.err);
-          else if (line.piece > 0) ok = twait(s, &s.o_free, uint32_t(line.piece - 1) & 1, a.err);
-          // the output of the piece before is out: its NaN positions make room for another's
-          if (!qk && ok && line.piece > 0)
-            for (int e = 0; e < 8; ++e) s.nan_at[(line.piece - 1) & (kNanSlots - 1)][e] = kVerNone;
-        }
-        if (!ok || !twait(s, qk ? &s.kfull[st] : &s.vfull[st], uint32_t(k >> 1) & 1, a.err)) break;
+        const uint32_t phase = uint32_t(k >> 1) & 1;
+        const uint32_t sp = tmem + kVerChunk * st;
         const uint64_t desc = desc0 + uint32_t(st * kTile >> 4);
-        for (int h = 0; h < subs && ok; ++h, ++sub) {
-          const int buf = sub & (kTBufs - 1);
-          const uint32_t sp = tmem + kTSub * buf;
-          if (qk) {
-            if (sub >= kTBufs && !twait(s, &s.p_free[buf], uint32_t(sub / kTBufs - 1) & 1, a.err)) { ok = false; break; }
-            tc_fence_after();
+        if (!twait_warp(s, qk ? &s.kfull[st] : &s.vfull[st], phase, a.err)) { ok = false; break; }
+        if (qk) {
+          if (k >= 2 && !twait_warp(s, &s.p_free[st], phase ^ 1, a.err)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ta(sp, tmem + kTQ + 8 * kk,
-                          desc + uint32_t(((kk >> 2) * kHalf + (kk & 3) * 32 + h * kTSub * 128) >> 4), idesc_f16(kTSub, false),
-                          kk > 0);
-            mma_commit(&s.s_full[buf]);
-          } else {
-            if (!twait(s, &s.p_full[buf], uint32_t(sub / kTBufs) & 1, a.err)) { ok = false; break; }
-            tc_fence_after();
+              mma_bf16_ta(sp, tmem + kTQ + 8 * kk, desc + uint32_t(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
+                          idesc_f16(kVerChunk, false), kk > 0);
+            mma_commit(&s.s_full[st]);
+            mma_commit(&s.kempty[st]);
+          }
+          __syncwarp();
+        } else {
 #pragma unroll
-            for (int kk = 0; kk < kTSub / 16; ++kk)
-              mma_bf16_ta(tmem + kTO, sp + 8 * kk, desc + uint32_t((h * kTSub + kk * 16) * 128 >> 4), idesc_f16(D, true),
-                          !(first && h == 0 && kk == 0));
-            mma_commit(&s.p_free[buf]);
+          for (int h = 0; h < 2; ++h) {
+            if (!twait_warp(s, &s.p_full[2 * st + h], phase, a.err)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kTSub / 16; ++kk)
+                mma_bf16_ta(tmem + kTO, sp + 32 * h + 8 * kk, desc + uint32_t((h * kTSub + kk * 16) * 128 >> 4),
+                            idesc_f16(D, true), h == 1 || kk > 0 || c > 0);
+              if (h == 0) {
+                mma_commit(&s.h_done);
+              } else {
+                mma_commit(&s.p_free[st]);
+                mma_commit(&s.vempty[st]);
+                if (c == n - 1) mma_commit(&s.o_full);
+              }
+            }
+            __syncwarp();
           }
         }
-        if (!ok) break;
-        mma_commit(qk ? &s.kempty[st] : &s.vempty[st]);
-        if (!qk && last) mma_commit(&s.o_full);
-        // (one thread walks the line: ver_next needs no other lane)
-        line_step(a, line);
       }
     }
   } else if (warp < act) {
     // ---------------------------------------------------------------- softmax and output
-    TLine line;
-    line_begin(a, line);
+    VerCursor cur = ver_begin(a, blockIdx.x);
+    VerPiece p;
     const int m = warp * 32 + lane, i = m / a.grp, j = m - i * a.grp;
     const uint32_t trow = tmem + (uint32_t(32 * warp) << 16);
-    int sub = 0;
+    int k = 0;
     bool ok = true;
-    while (line.live && ok) {
-      const VerPiece p = line.p;
-      const int piece = line.piece;
+    for (int piece = 0; ok && ver_next(a, cur, p); ++piece) {
       // the row's queries, scaled by a power of two, in the tiles' column order
       const bool real = m < a.M && i < p.rows;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (int64_t(p.b) * a.n_rows + i) * a.q_stride +
@@ -408,16 +416,19 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
       mbar_arrive(&s.q_full);
 
       float ref = -INFINITY, sum = 0.f;
-      const int64_t limit = min(p.len, ver_limit(p, i));
-      for (int64_t c = p.c0; c < p.c1 && ok; ++c) {
-        const int subs = p.len - c * kVerChunk > kTSub ? 2 : 1;
-        for (int h = 0; h < subs; ++h, ++sub) {
-          const int buf = sub & (kTBufs - 1);
-          const int64_t pos0 = c * kVerChunk + h * kTSub;
-          if (!twait_warp(s, &s.s_full[buf], uint32_t(sub / kTBufs) & 1, a.err)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sp = trow + kTSub * buf;
-          const int seen = limit - pos0 >= kTSub ? kTSub : (limit > pos0 ? int(limit - pos0) : 0);
+      const int n = int(p.c1 - p.c0);
+      // keys this row sees from the piece's first on
+      const int64_t span = min(p.len, ver_limit(p, i)) - p.c0 * kVerChunk;
+      const int limit = span > (int64_t(1) << 30) ? 1 << 30 : (span < 0 ? 0 : int(span));
+      for (int c = 0; c < n && ok; ++c, ++k) {
+        const int st = k & 1;
+        const uint32_t phase = uint32_t(k >> 1) & 1;
+        if (!twait_warp(s, &s.s_full[st], phase, a.err)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t sp = trow + kVerChunk * st + kTSub * h;
+          const int seen = limit - (c * kVerChunk + h * kTSub);
           const bool edge = __any_sync(0xffffffffu, seen < kTSub);
           float x[64], part;
           auto weigh = [&]() {  // x: weights against ref; part: their sum
@@ -450,8 +461,13 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
             const float al = nref == ref ? 1.f : ex2a(ref - nref);
             ref = nref;
             sum *= al;
-            if (c > p.c0 || h > 0) {  // O holds the sub-chunks before this one
-              if (!twait_warp(s, &s.p_free[(sub - 1) & (kTBufs - 1)], uint32_t((sub - 1) / kTBufs) & 1, a.err)) { ok = false; break; }
+            if (c > 0 || h > 0) {  // O holds the keys before these, once their P V has landed
+              if (h == 0) {
+                ok = twait_warp(s, &s.p_free[st ^ 1], uint32_t((k - 1) >> 1) & 1, a.err);
+              } else {
+                ok = twait_warp(s, &s.h_done, uint32_t(k) & 1, a.err);
+              }
+              if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
               for (int h2 = 0; h2 < D / 32; ++h2) {
@@ -468,9 +484,9 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
           uint32_t w[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) w[e] = pack_half2(x[2 * e], x[2 * e + 1]);
-          tmem_st32u(sp, w);
+          tmem_st32u(trow + kVerChunk * st + 32 * h, w);
           tc_fence_before();
-          mbar_arrive(&s.p_full[buf]);
+          mbar_arrive(&s.p_full[2 * st + h]);
         }
       }
       if (!ok || !twait_warp(s, &s.o_full, uint32_t(piece) & 1, a.err)) break;
@@ -514,16 +530,16 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
       }
       tc_fence_before();
       mbar_arrive(&s.o_free);
-      line.piece = piece + 1;
-      line.live = ver_next(a, line.cur, line.p);
-      line.c = line.p.c0;
     }
   }
 
   __syncthreads();
-  if ((warp == 12 || warp == 13) && lane == 0 && s.abort) {  // the MMAs issued so far, before TMEM is freed
-    mma_commit(&s.drain[warp - 12]);
-    mbar_wait_bounded(&s.drain[warp - 12], 0, kWaitLimit);
+  if ((warp == 12 || warp == 13) && s.abort) {  // the MMAs issued so far, before TMEM is freed
+    if (elect_one()) {
+      mma_commit(&s.drain[warp - 12]);
+      mbar_wait_bounded(&s.drain[warp - 12], 0, kWaitLimit);
+    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
