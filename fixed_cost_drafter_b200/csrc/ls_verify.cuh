@@ -183,6 +183,24 @@ __device__ inline int64_t ver_out_at(const VerArgs& a, int b, int i, int h) {
   return ((int64_t(b) * a.n_rows + i) * a.Hq + h) * a.D;
 }
 
+// Bounded wait of a whole warp; S holds the CTA's abort flag. Every lane polls: a whole warp's
+// try_wait sleeps until the phase completes, one lane's comes back after about 200 cycles and
+// polls again (a wait for a complete phase costs about 200 cycles either way).
+template <typename S>
+__device__ inline bool ver_wait_warp(S& s, uint64_t* bar, uint32_t parity, int32_t* err) {
+  bool ok = false;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    ok = mbar_try_wait(bar, parity);
+    if (ok || ((i & 1023) == 1023 && *reinterpret_cast<volatile uint32_t*>(&s.abort))) break;
+  }
+  if (!ok) {
+    if (!*reinterpret_cast<volatile uint32_t*>(&s.abort)) set_err(err, LS_DEVERR_WAIT_TIMEOUT);
+    *reinterpret_cast<volatile uint32_t*>(&s.abort) = 1;
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 // A launch that may start while the kernel before it on the stream still runs: the kernels here
 // wait for it (grid_dependency_wait) before they read or write anything.
 template <typename... A>

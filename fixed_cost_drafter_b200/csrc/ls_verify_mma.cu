@@ -67,18 +67,6 @@ __device__ inline float exp2_approx(float x) {
 }
 __device__ inline void consumers_meet() { asm volatile("bar.sync 1, %0;" ::"n"(kMWarps * 32) : "memory"); }
 
-template <typename S>
-__device__ inline bool ver_wait(S& s, uint64_t* bar, uint32_t parity, int32_t* err) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 1023) == 1023 && *reinterpret_cast<volatile uint32_t*>(&s.abort)) return false;
-  }
-  set_err(err, LS_DEVERR_WAIT_TIMEOUT);
-  *reinterpret_cast<volatile uint32_t*>(&s.abort) = 1;
-  return false;
-}
-
 template <int NT, int D>
 __global__ void __launch_bounds__(kMThreads) verify_mma_kernel(const VerArgs a) {
   constexpr int kSteps = D / 16;        // k16 steps of Q K^T; also registers pairs of Q per n-tile
@@ -120,7 +108,7 @@ __global__ void __launch_bounds__(kMThreads) verify_mma_kernel(const VerArgs a) 
         if (c + 1 < p.c1) next = block_of(c + 1);
         const int st = k % kMStages;
         if (k >= kMStages &&
-            !__all_sync(0xffffffffu, ver_wait(s, &s.empty[st], uint32_t(k / kMStages - 1) & 1, a.err))) {
+            !ver_wait_warp(s, &s.empty[st], uint32_t(k / kMStages - 1) & 1, a.err)) {
           ok = false;
           break;
         }
@@ -209,7 +197,7 @@ __global__ void __launch_bounds__(kMThreads) verify_mma_kernel(const VerArgs a) 
 
     for (int64_t c = p.c0; c < p.c1; ++c, ++k) {
       const int st = k % kMStages;
-      if (ok && !__all_sync(0xffffffffu, ver_wait(s, &s.full[st], uint32_t(k / kMStages) & 1, a.err))) ok = false;
+      if (ok && !ver_wait_warp(s, &s.full[st], uint32_t(k / kMStages) & 1, a.err)) ok = false;
       if (!ok) continue;
       const unsigned char* base = ring + st * stage_bytes(D);
       const bool edge = (c + 1) * kVerChunk > full_seen;

@@ -4,24 +4,31 @@
 // What bounds it: at 68 rows the two products (128 rows x 128 keys x D each, tcgen05 f16) take
 // about as long as the bytes of the cache take to arrive, and the operands have to be made
 // first: shared memory carries every fp16 operand twice (written by the conversion, read by
-// the MMA). So nothing else goes through shared memory: codes come from global memory straight
-// into the converting threads' registers, two chunks ahead, and Q and the weights P are the
-// MMAs' A operands in TMEM.
+// the MMA). So what can stays out of it: Q and the weights P are the MMAs' A operands in TMEM.
+// The codes do go through it, as bulk copies: loaded straight into the converting threads'
+// registers, two units of 16 rows ahead, every use of a loaded value waited for the newest
+// loads as well (about 3000 cycles a unit).
 //
-// One CTA per SM, 14 warps; the roles meet at mbarriers:
-//   warps 4-11  conversion: warp w takes 16 rows of each 128-key chunk, a thread 16 codes (one
-//               scale group) at a time; K and V tiles in the 128-byte swizzle, two buffers
-//               each. A group's two 16-byte pieces go to different 64-column halves (D = 128),
-//               so that eight threads fill a whole 128-byte row; Q and the output columns
-//               follow the same order.
-//   warp 12     S = Q K^T of a chunk into one of two 128-column buffers (8 MMAs of N = 128: an
+// One CTA per SM, 16 warps; the roles meet at mbarriers:
+//   warp 10     producer: a chunk's pages into a ring of 4 stages (the page's block of a KV head
+//               is one copy)
+//   warps 11-15 conversion, with the softmax warps that have no rows (68 rows leave two idle, in
+//               the SM sub-partition that then has no softmax at all): tasks of 32 rows of a
+//               chunk's K or V, round robin, a thread 16 codes (one scale group) at a time; tiles
+//               in the 128-byte swizzle, two buffers each. A group's two 16-byte pieces go to
+//               different 64-column halves (D = 128), so that eight threads fill a whole 128-byte
+//               row; Q and the output columns follow the same order.
+//   warp 8      S = Q K^T of a chunk into one of two 128-column buffers (8 MMAs of N = 128: an
 //               MMA costs its issuing thread about 80 cycles whatever its N)
-//   warps 0-3   softmax, a thread per query row, 64 keys at a time: weights 2^(x - r) in fp16,
+//   warps 0-7   softmax, a thread per query row, 64 keys at a time: weights 2^(x - r) in fp16,
 //               written over S. The reference r only moves when 64 weights sum to more than
 //               2^15 (fp16 holds up to 65504); it is then the maximum less 8, as in
 //               ls_verify_mma.cu, and the row of O is scaled in TMEM. The sum is needed anyway:
-//               the check costs no maximum.
-//   warp 13     O += P V, 64 keys at a time
+//               the check costs no maximum. Warps 0-3 take the even chunks, 4-7 the odd ones
+//               (a lone warp per SM sub-partition waits out every latency: 522 us instead of
+//               the figure below); one O needs one reference, so a warp passes it on with each
+//               chunk and takes the other's up before it writes its weights.
+//   warp 9      O += P V, 64 keys at a time
 // TMEM columns: S / P 0-255, O 256-383, Q 384-447.
 // Rounding, exactness of the held values and NaN groups: as in ls_verify_mma.cu.
 #include "ls_verify.cuh"
@@ -31,8 +38,11 @@ namespace ls {
 
 namespace {
 
-constexpr int kTThreads = 448;
-constexpr int kTConv = 8;          // conversion warps
+constexpr int kTThreads = 512;
+constexpr int kTQkWarp = 8, kTPvWarp = 9, kTLoadWarp = 10, kTConvWarp = 11;
+constexpr int kTRing = 4;          // stages of raw chunks
+constexpr int kTUnit = 32;         // rows of a conversion task
+constexpr int kTUnits = kVerChunk / kTUnit;  // of a chunk's keys, and as many of its values
 constexpr int kTSub = 64;          // keys the softmax takes at a time
 constexpr uint32_t kTCols = 512, kTO = 256, kTQ = 384;
 constexpr float kTRoom = 8.f;
@@ -40,27 +50,18 @@ constexpr float kTMostSum = 32768.f;
 constexpr int kNanSlots = 4;       // pieces whose NaN positions are kept (conversion runs at most 2 ahead)
 
 struct TBars {
+  uint64_t raw_full[kTRing], raw_empty[kTRing];
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t s_full[2], p_full[4], p_free[2];  // p_full: [buffer][half]
   uint64_t h_done;  // the first half's P V
+  uint64_t decided[4][2];  // per softmax warp pair: the reference after an even / odd chunk
+  uint64_t joined[4];      // both warps' sums of a piece
   uint64_t q_full, o_full, o_free, drain[2];
   uint32_t tmem_base, abort;
   int nan_at[kNanSlots][8];
+  float ref[kTcRows];
+  float2 state[2][2][kTcRows];  // [piece parity][warp group]: sum and reference of a row
 };
-
-__device__ inline bool twait(TBars& s, uint64_t* bar, uint32_t parity, int32_t* err) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 1023) == 1023 && *reinterpret_cast<volatile uint32_t*>(&s.abort)) return false;
-  }
-  set_err(err, LS_DEVERR_WAIT_TIMEOUT);
-  *reinterpret_cast<volatile uint32_t*>(&s.abort) = 1;
-  return false;
-}
-__device__ inline bool twait_warp(TBars& s, uint64_t* bar, uint32_t parity, int32_t* err) {
-  return __all_sync(0xffffffffu, twait(s, bar, parity, err));
-}
 
 // kind::f16 with fp16 A/B, fp32 D
 constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
@@ -73,25 +74,6 @@ __device__ inline bool elect_one() {
   return r != 0;
 }
 
-__device__ inline void tmem_ld64(uint32_t taddr, float (&v)[64]) {
-  uint32_t r[64];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[32 * h + 0]), "=r"(r[32 * h + 1]), "=r"(r[32 * h + 2]), "=r"(r[32 * h + 3]), "=r"(r[32 * h + 4]),
-          "=r"(r[32 * h + 5]), "=r"(r[32 * h + 6]), "=r"(r[32 * h + 7]), "=r"(r[32 * h + 8]), "=r"(r[32 * h + 9]),
-          "=r"(r[32 * h + 10]), "=r"(r[32 * h + 11]), "=r"(r[32 * h + 12]), "=r"(r[32 * h + 13]), "=r"(r[32 * h + 14]),
-          "=r"(r[32 * h + 15]), "=r"(r[32 * h + 16]), "=r"(r[32 * h + 17]), "=r"(r[32 * h + 18]), "=r"(r[32 * h + 19]),
-          "=r"(r[32 * h + 20]), "=r"(r[32 * h + 21]), "=r"(r[32 * h + 22]), "=r"(r[32 * h + 23]), "=r"(r[32 * h + 24]),
-          "=r"(r[32 * h + 25]), "=r"(r[32 * h + 26]), "=r"(r[32 * h + 27]), "=r"(r[32 * h + 28]), "=r"(r[32 * h + 29]),
-          "=r"(r[32 * h + 30]), "=r"(r[32 * h + 31])
-        : "r"(taddr + 32 * h));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
-}
 __device__ inline void tmem_st32u(uint32_t taddr, const uint32_t* v) {
   tmem_st32(taddr, reinterpret_cast<const float*>(v));
 }
@@ -130,38 +112,49 @@ __device__ constexpr int dim_of(int n) {
 template <int D>
 __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a) {
   constexpr int kTile = kVerChunk * D * 2;     // one K or V buffer
+  constexpr int kRaw = kVerChunk * (D + D / 8);  // a raw chunk
   constexpr int kHalf = kVerChunk * 128;       // 64 columns of it
   constexpr int kGroups = D / kKv4Group;       // threads per row in the conversion
-  constexpr int kRowStep = 32 / kGroups, kIter = 16 / kRowStep;
+  constexpr int kRowStep = 32 / kGroups, kIter = kTUnit / kRowStep;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ TBars s;
   unsigned char* kbuf = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* vbuf = kbuf + 2 * kTile;
+  unsigned char* ring = vbuf + 2 * kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int act = (a.M + 31) / 32;             // softmax warps with rows
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kTRing; ++i) {
+      mbar_init(&s.raw_full[i], 1);
+      mbar_init(&s.raw_empty[i], 2 * kTUnits);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.kfull[i], kTConv);
+      mbar_init(&s.kfull[i], kTUnits);
       mbar_init(&s.kempty[i], 1);
-      mbar_init(&s.vfull[i], kTConv);
+      mbar_init(&s.vfull[i], kTUnits);
       mbar_init(&s.vempty[i], 1);
       mbar_init(&s.drain[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[2 * i], 32 * act);
-      mbar_init(&s.p_full[2 * i + 1], 32 * act);
+      mbar_init(&s.p_full[2 * i], act);
+      mbar_init(&s.p_full[2 * i + 1], act);
       mbar_init(&s.p_free[i], 1);
     }
-    mbar_init(&s.q_full, 32 * act);
+    mbar_init(&s.q_full, act);
     mbar_init(&s.o_full, 1);
     mbar_init(&s.h_done, 1);
-    mbar_init(&s.o_free, 32 * act);
+    mbar_init(&s.o_free, 2 * act);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s.decided[i][0], 1);
+      mbar_init(&s.decided[i][1], 1);
+      mbar_init(&s.joined[i], 2);
+    }
     s.abort = 0;
     for (int i = 0; i < kNanSlots * 8; ++i) s.nan_at[i >> 3][i & 7] = kVerNone;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == kTQkWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem_base)),
                  "r"(kTCols)
                  : "memory");
@@ -174,77 +167,29 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
   grid_dependency_wait();
   allow_dependent_launch();
 
-  if (warp >= 4 && warp < 12) {
+  const bool idle = warp < kTQkWarp && (warp & 3) >= act;  // a softmax warp without rows
+  if (warp >= kTConvWarp || idle) {
     // ---------------------------------------------------------------- conversion
-    const int cw = warp - 4, row0 = cw * 16;
+    // Every second of them takes keys, the others values. The values' buffers wait for the
+    // weights' use of them, which must not hold up the next scores' keys; and a barrier's parity
+    // names a phase only while the one before is known to be complete and the one behind cannot
+    // be: a warp's tasks of one kind lie at most two chunks apart (at most 2 kTUnits warps), and
+    // the products of a chunk wait for its tasks.
+    const int spare = kTThreads / 32 - kTConvWarp;
+    const int index = idle ? spare + ((warp & 3) - act) * 2 + (warp >> 2) : warp - kTConvWarp;
+    const int v = index & 1, me = index >> 1;
+    const int n_conv = min((spare + 2 * (4 - act) + 1 - v) / 2, 2 * kTUnits);
+    uint64_t* const empty = v ? s.vempty : s.kempty;
+    uint64_t* const full = v ? s.vfull : s.kfull;
+    unsigned char* const buf = v ? vbuf : kbuf;
     const int r = lane / kGroups, g = lane % kGroups;  // this thread's row (of kRowStep) and group
-    const int ps = a.page_size;
+    const int ps = min(a.page_size, kVerChunk), pshift = min(a.page_shift, 7);  // rows per block of a stage
     VerCursor cur = ver_begin(a, blockIdx.x);
-    const int total = int(cur.left);  // chunks of this CTA
-    // The lookup walks ahead of the conversion: the page of a chunk is looked up three chunks
-    // ahead, its codes are loaded two ahead.
     VerPiece p;
-    int64_t pos = 0;   // of this warp's 16 rows in the chunk looked up next
-    int left = 0, piece = -1, rel = 0;
-    int32_t entry = 0;
-    auto look_up = [&]() {
-      if (left == 0) {
-        if (!ver_next(a, cur, p)) return;
-        left = int(p.c1 - p.c0);
-        pos = p.c0 * kVerChunk + row0;
-        rel = row0;
-        ++piece;
-      }
-      entry = pos < p.len ? __ldg(a.table + int64_t(p.b) * a.max_blocks + (pos >> a.page_shift)) : 0;
-    };
-    struct Rows {  // a chunk's 16 rows of this warp: codes and scales in flight
-      uint2 w[2][kIter];
-      uint32_t sc[2][kIter];
-      int held, rel, piece;  // rows below the sequence's length, position in the piece, piece
-    };
-    Rows rows[2];
-    const unsigned char* src = nullptr;  // the chunk whose rows are loaded next: its keys' codes
-    int to_scales = 0;
-    const int code_at = r * (D / 2) + g * 8, scale_at = r * kGroups + g;
-    // the chunk looked up becomes the next to load, and the one behind it is looked up
-    auto resolve = [&](Rows& q) {
-      src = nullptr;
-      q.held = 0;
-      if (left > 0) {
-        if (pos < p.len) {
-          int64_t page = entry;
-          if (page < 0 || page >= a.num_pages) {
-            set_err(a.err, LS_DEVERR_PAGE);
-            page = 0;
-          }
-          const int off = int(pos) & (ps - 1);
-          src = a.base + page * a.page_stride + int64_t(p.hm) * kv4_block_bytes(ps, D) + off * (D / 2);
-          to_scales = ps * D + off * (D / kKv4Group) - off * (D / 2);
-          q.held = p.len - pos < 16 ? int(p.len - pos) : 16;
-        }
-        q.rel = rel;
-        q.piece = piece & (kNanSlots - 1);
-        pos += kVerChunk;
-        rel += kVerChunk;
-        --left;
-      }
-      look_up();
-    };
-    auto load = [&](Rows& q, int v) {
-      const unsigned char* c = src + v * ps * (D / 2) + code_at;
-      const unsigned char* sp = src + to_scales + v * ps * (D / kKv4Group) + scale_at;
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        q.w[v][i] = make_uint2(0u, 0u);
-        q.sc[v][i] = 0u;
-        if (src) {
-          asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                       : "=r"(q.w[v][i].x), "=r"(q.w[v][i].y)
-                       : "l"(c + i * kRowStep * (D / 2)));
-          asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(q.sc[v][i]) : "l"(sp + i * kRowStep * kGroups));
-        }
-      }
-    };
+    // next task: unit `task` of the chunk; chunks of the piece from that one on; its first position
+    // in the piece; its sequence's rows from there on
+    int task = me, chunk = 0, left = 0, piece = -1, rel = 0;
+    int64_t held = 0;
     // the thread's 16 codes of a row as two 16-byte pieces of the tile
     auto put = [&](unsigned char* line0, const uint2& w, uint32_t scale) {
       const uint32_t s2 = e4m3x2_to_half2(uint16_t(scale * 0x101u));
@@ -259,61 +204,121 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
                                        : reinterpret_cast<unsigned char*>(reinterpret_cast<uintptr_t>(line0) ^ 16);
       *reinterpret_cast<uint4*>(second) = make_uint4(h[4], h[5], h[6], h[7]);
     };
-    // the first piece's place in the thread's rows: row0 + r + i kRowStep; 8 rows apart the
-    // swizzle repeats
-    int place[kIter];
+    // the first piece's place in row r of a task; 8 rows on the swizzle repeats
+    constexpr int kPlaces = kRowStep < 8 ? 8 / kRowStep : 1;
+    int place[kPlaces];
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-      const int row = row0 + r + i * kRowStep;
+    for (int i = 0; i < kPlaces; ++i) {
+      const int row = r + i * kRowStep;
       place[i] = row * 128 + (((D == 128 ? g : 2 * g) ^ (row & 7)) << 4);
     }
-    look_up();
+    while (me < n_conv) {
+      if (left == 0) {
+        if (!ver_next(a, cur, p)) break;
+        left = int(p.c1 - p.c0);
+        held = p.len - p.c0 * kVerChunk;
+        rel = 0;
+        ++piece;
+      }
+      if (task >= kTUnits) {
+        task -= kTUnits;
+        ++chunk;
+        --left;
+        held -= kVerChunk;
+        rel += kVerChunk;
+        continue;
+      }
+      const int row0 = task * kTUnit, st = chunk & 1, rs = chunk % kTRing;
+      // codes and scales of the rows' two blocks of 16
+      const unsigned char *codes[2], *scales[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      resolve(rows[i]);
-      load(rows[i], 0);
-      load(rows[i], 1);
-    }
-    bool ok = true;
-    for (int k0 = 0; k0 < total && ok; k0 += 2) {
+      for (int x = 0; x < 2; ++x) {
+        const int row = row0 + 16 * x;
+        const unsigned char* blk = ring + rs * kRaw + (row >> pshift) * kv4_block_bytes(ps, D);
+        const int off = (row & (ps - 1)) + v * ps + r;
+        codes[x] = blk + off * (D / 2) + g * 8;
+        scales[x] = blk + ps * D + off * kGroups + g;
+      }
+      if (!ver_wait_warp(s, &s.raw_full[rs], uint32_t(chunk / kTRing) & 1, a.err)) break;
+      uint2 w[kIter];
+      uint32_t sc[kIter];
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const int k = k0 + st;
-        if (k >= total) break;
-        Rows& q = rows[st];
-        const int held = q.held, at = q.rel, slot = q.piece;
-        resolve(q);  // chunk k + 2
-        if (k >= 2 && !twait_warp(s, &s.kempty[st], uint32_t((k >> 1) - 1) & 1, a.err)) { ok = false; break; }
-#pragma unroll
-        for (int i = 0; i < kIter; ++i) put(kbuf + st * kTile + place[i], q.w[0][i], q.sc[0][i]);
-        load(q, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.kfull[st]);
+      for (int i = 0; i < kIter; ++i) {
+        w[i] = *reinterpret_cast<const uint2*>(codes[i / (kIter / 2)] + (i % (kIter / 2)) * kRowStep * (D / 2));
+        sc[i] = scales[i / (kIter / 2)][(i % (kIter / 2)) * kRowStep * kGroups];
+      }
+      if (chunk >= 2 && !ver_wait_warp(s, &empty[st], uint32_t((chunk >> 1) - 1) & 1, a.err)) break;
+      if (v) {
         bool nan = false;
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) nan |= nan_scale(q.sc[1][i]);
-        if (nan) {  // such a group takes part as zeros (ls_verify.cuh)
+        for (int i = 0; i < kIter; ++i) nan |= nan_scale(sc[i]);
+        // such a group takes part as zeros (ls_verify.cuh). Its slot is free: P V two chunks back
+        // is done, so the output of the piece three chunks back is out
+        if (nan) {
 #pragma unroll
           for (int i = 0; i < kIter; ++i) {
-            if (!nan_scale(q.sc[1][i])) continue;
-            if (r + i * kRowStep < held) atomicMin(&s.nan_at[slot][g], at + r + i * kRowStep);
-            q.sc[1][i] = 0u;
+            if (!nan_scale(sc[i])) continue;
+            const int row = row0 + r + i * kRowStep;
+            if (row < held) atomicMin(&s.nan_at[piece & (kNanSlots - 1)][g], rel + row);
+            sc[i] = 0u;
           }
         }
-        if (k >= 2 && !twait_warp(s, &s.vempty[st], uint32_t((k >> 1) - 1) & 1, a.err)) { ok = false; break; }
+      }
+      unsigned char* tile = buf + st * kTile + row0 * 128;
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) put(vbuf + st * kTile + place[i], q.w[1][i], q.sc[1][i]);
-        load(q, 1);
-        fence_proxy_async_smem();
+      for (int i = 0; i < kIter; ++i) put(tile + place[i & (kPlaces - 1)] + (i / kPlaces) * (kPlaces * kRowStep * 128), w[i], sc[i]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&full[st]);
+        mbar_arrive(&s.raw_empty[rs]);  // the task's codes are read
+      }
+      task += n_conv;
+    }
+  } else if (warp == kTLoadWarp) {
+    // ---------------------------------------------------------------- producer
+    const int ps = min(a.page_size, kVerChunk), pshift = min(a.page_shift, 7);
+    const bool wide = a.page_size > kVerChunk;  // a chunk is half of a 256-row page: its four sections
+    const int lanes = wide ? 4 : kVerChunk >> pshift;
+    VerCursor cur = ver_begin(a, blockIdx.x);
+    VerPiece p;
+    int k = 0;
+    bool ok = true;
+    while (ok && ver_next(a, cur, p)) {
+      auto block_of = [&](int64_t c) -> const unsigned char* {  // this lane's page of a chunk
+        const int64_t pos = c * kVerChunk + (wide ? 0 : int64_t(lane) << pshift);
+        return lane < lanes && pos < p.len ? ver_block(a, p.b, pos >> a.page_shift, p.hm) : nullptr;
+      };
+      const unsigned char* next = block_of(p.c0);
+      for (int64_t c = p.c0; c < p.c1; ++c, ++k) {
+        const unsigned char* block = next;
+        if (c + 1 < p.c1) next = block_of(c + 1);
+        const int rs = k % kTRing;
+        if (k >= kTRing && !ver_wait_warp(s, &s.raw_empty[rs], uint32_t(k / kTRing - 1) & 1, a.err)) { ok = false; break; }
+        unsigned char* dst = ring + rs * kRaw;
+        const int n = __popc(__ballot_sync(0xffffffffu, block != nullptr));
+        if (lane == 0) mbar_arrive_expect_tx(&s.raw_full[rs], uint32_t(wide ? kRaw : n * kv4_block_bytes(ps, D)));
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.vfull[st]);
+        if (wide) {
+          if (lane < 4) {  // 128 of the page's rows: codes (lanes 0, 1) and scales (2, 3)
+            const int row = lane < 2 ? D / 2 : D / kKv4Group, bytes = kVerChunk * row;
+            const int64_t from = (lane < 2 ? 0 : int64_t(a.page_size) * D) + int64_t(lane & 1) * a.page_size * row +
+                                 (c * kVerChunk & (a.page_size - 1)) * row;
+            bulk_g2s(dst + (lane < 2 ? 0 : kVerChunk * D) + (lane & 1) * bytes, block + from, bytes, &s.raw_full[rs]);
+          }
+        } else if (block) {
+          bulk_g2s(dst + lane * kv4_block_bytes(ps, D), block, kv4_block_bytes(ps, D), &s.raw_full[rs]);
+        }
       }
     }
-  } else if (warp == 12 || warp == 13) {
+    // after an abort: the copies in flight land before the shared memory is released
+    if (lane == 0 && *reinterpret_cast<volatile uint32_t*>(&s.abort))
+      for (int x = k > kTRing ? k - kTRing : 0; x < k; ++x)
+        mbar_wait_bounded(&s.raw_full[x % kTRing], uint32_t(x / kTRing) & 1, kWaitLimit);
+  } else if (warp == kTQkWarp || warp == kTPvWarp) {
     // ---------------------------------------------------------------- MMA issuers
     // the whole warp walks the chunks; one elected lane issues
-    const bool qk = warp == 12;
+    const bool qk = warp == kTQkWarp;
     VerCursor cur = ver_begin(a, blockIdx.x);
     VerPiece p;
     const uint64_t desc0 = qk ? sdesc(smem_u32(kbuf), 16, 1024) : sdesc(smem_u32(vbuf), kHalf, 1024);
@@ -322,9 +327,9 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
     for (int piece = 0; ok && ver_next(a, cur, p); ++piece) {
       const int n = int(p.c1 - p.c0);
       if (qk) {
-        ok = twait_warp(s, &s.q_full, uint32_t(piece) & 1, a.err);
+        ok = ver_wait_warp(s, &s.q_full, uint32_t(piece) & 1, a.err);
       } else if (piece > 0) {
-        ok = twait_warp(s, &s.o_free, uint32_t(piece - 1) & 1, a.err);
+        ok = ver_wait_warp(s, &s.o_free, uint32_t(piece - 1) & 1, a.err);
         // the output of the piece before is out: its NaN positions make room for another's
         if (lane < 8) s.nan_at[(piece - 1) & (kNanSlots - 1)][lane] = kVerNone;
         __syncwarp();
@@ -334,9 +339,9 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
         const uint32_t phase = uint32_t(k >> 1) & 1;
         const uint32_t sp = tmem + kVerChunk * st;
         const uint64_t desc = desc0 + uint32_t(st * kTile >> 4);
-        if (!twait_warp(s, qk ? &s.kfull[st] : &s.vfull[st], phase, a.err)) { ok = false; break; }
+        if (!ver_wait_warp(s, qk ? &s.kfull[st] : &s.vfull[st], phase, a.err)) { ok = false; break; }
         if (qk) {
-          if (k >= 2 && !twait_warp(s, &s.p_free[st], phase ^ 1, a.err)) { ok = false; break; }
+          if (k >= 2 && !ver_wait_warp(s, &s.p_free[st], phase ^ 1, a.err)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!twait_warp(s, &s.p_full[2 * st + h], phase, a.err)) { ok = false; break; }
+            if (!ver_wait_warp(s, &s.p_full[2 * st + h], phase, a.err)) { ok = false; break; }
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -370,12 +375,13 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
         }
       }
     }
-  } else if (warp < act) {
+  } else {
     // ---------------------------------------------------------------- softmax and output
+    const int grp = warp >> 2, wp = warp & 3;  // warp group: even or odd chunks; its 32 rows
     VerCursor cur = ver_begin(a, blockIdx.x);
     VerPiece p;
-    const int m = warp * 32 + lane, i = m / a.grp, j = m - i * a.grp;
-    const uint32_t trow = tmem + (uint32_t(32 * warp) << 16);
+    const int m = wp * 32 + lane, i = m / a.grp, j = m - i * a.grp;
+    const uint32_t trow = tmem + (uint32_t(32 * wp) << 16);
     int k = 0;
     bool ok = true;
     for (int piece = 0; ok && ver_next(a, cur, p); ++piece) {
@@ -396,24 +402,27 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
       int ex = int(__float_as_uint(top) >> 23) - 127;
       if (top == 0.f || ex > 127) ex = 0;
       if (ex < -126) ex = -126;
-      const float down = ex == 127 ? 0x1p-127f : __uint_as_float(uint32_t(127 - ex) << 23);
       const float f = ldexpf(a.scale_log2, ex);
+      if (grp == 0) {
+        const float down = ex == 127 ? 0x1p-127f : __uint_as_float(uint32_t(127 - ex) << 23);
+#pragma unroll 1
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t w[32];
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        uint32_t w[32];
+          for (int c8 = 0; c8 < 8; ++c8) {
+            float x[8];
 #pragma unroll
-        for (int c8 = 0; c8 < 8; ++c8) {
-          float x[8];
+            for (int u = 0; u < 8; ++u) x[u] = 0.f;
+            if (real) Elem<__nv_bfloat16>::to_f32(ld_nc_v4(src + dim_of<D>(64 * h + 8 * c8)), x);
 #pragma unroll
-          for (int u = 0; u < 8; ++u) x[u] = 0.f;
-          if (real) Elem<__nv_bfloat16>::to_f32(ld_nc_v4(src + dim_of<D>(64 * h + 8 * c8)), x);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) w[4 * c8 + u] = pack_half2(x[2 * u] * down, x[2 * u + 1] * down);
+            for (int u = 0; u < 4; ++u) w[4 * c8 + u] = pack_half2(x[2 * u] * down, x[2 * u + 1] * down);
+          }
+          tmem_st32u(trow + kTQ + 32 * h, w);
         }
-        tmem_st32u(trow + kTQ + 32 * h, w);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.q_full);
       }
-      tc_fence_before();
-      mbar_arrive(&s.q_full);
 
       float ref = -INFINITY, sum = 0.f;
       const int n = int(p.c1 - p.c0);
@@ -421,54 +430,66 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
       const int64_t span = min(p.len, ver_limit(p, i)) - p.c0 * kVerChunk;
       const int limit = span > (int64_t(1) << 30) ? 1 << 30 : (span < 0 ? 0 : int(span));
       for (int c = 0; c < n && ok; ++c, ++k) {
-        const int st = k & 1;
+        if ((k & 1) != grp) continue;
         const uint32_t phase = uint32_t(k >> 1) & 1;
-        if (!twait_warp(s, &s.s_full[st], phase, a.err)) { ok = false; break; }
+        if (!ver_wait_warp(s, &s.s_full[grp], phase, a.err)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          const uint32_t sp = trow + kVerChunk * st + kTSub * h;
+          const uint32_t sp = trow + kVerChunk * grp + kTSub * h;
           const int seen = limit - (c * kVerChunk + h * kTSub);
           const bool edge = __any_sync(0xffffffffu, seen < kTSub);
-          float x[64], part;
-          auto weigh = [&]() {  // x: weights against ref; part: their sum
-            const float mu = -ref;
-            float acc[8];
+          uint32_t w[32];
+          float part;
+          auto weigh = [&]() {  // w: the 64 weights against ref; part: their sum
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+            for (int b = 0; b < 2; ++b) {
+              float x[32];
+              tmem_ld32(sp + 32 * b, x);
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) fma2(x[e], x[e + 1], f, mu);
-            if (edge) {
+              for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], f, -ref);
+              if (edge) {
 #pragma unroll
-              for (int e = 0; e < 64; ++e) x[e] = e < seen ? x[e] : -INFINITY;
-            }
-#pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              x[e] = ex2a(x[e]);
-              x[e + 1] = ex2a(x[e + 1]);
-              add2(acc[e & 6], acc[(e & 6) + 1], x[e], x[e + 1]);
-            }
-            part = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
-          };
-          tmem_ld64(sp, x);
-          weigh();
-          if (__any_sync(0xffffffffu, part > kTMostSum)) {
-            tmem_ld64(sp, x);
-            float mx = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 64; ++e) mx = fmaxf(mx, e < seen ? x[e] * f : -INFINITY);
-            const float nref = part > kTMostSum ? fmaxf(ref, mx - kTRoom) : ref;
-            const float al = nref == ref ? 1.f : ex2a(ref - nref);
-            ref = nref;
-            sum *= al;
-            if (c > 0 || h > 0) {  // O holds the keys before these, once their P V has landed
-              if (h == 0) {
-                ok = twait_warp(s, &s.p_free[st ^ 1], uint32_t((k - 1) >> 1) & 1, a.err);
-              } else {
-                ok = twait_warp(s, &s.h_done, uint32_t(k) & 1, a.err);
+                for (int e = 0; e < 32; ++e) x[e] = 32 * b + e < seen ? x[e] : -INFINITY;
               }
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                x[e] = ex2a(x[e]);
+                x[e + 1] = ex2a(x[e + 1]);
+                add2(acc[e & 2], acc[(e & 2) + 1], x[e], x[e + 1]);
+                w[16 * b + e / 2] = pack_half2(x[e], x[e + 1]);
+              }
+            }
+            part = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          };
+          weigh();
+          float now = ref;  // the row's reference so far
+          if (h == 0 && c > 0) {
+            if (!ver_wait_warp(s, &s.decided[wp][grp ^ 1], uint32_t((k - 1) >> 1) & 1, a.err)) { ok = false; break; }
+            now = s.ref[m];
+          }
+          const bool move = !(part <= kTMostSum) || now != ref;
+          if (__any_sync(0xffffffffu, move)) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+              float x[32];
+              tmem_ld32(sp + 32 * b, x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx = fmaxf(mx, 32 * b + e < seen ? x[e] * f : -INFINITY);
+            }
+            const float next = move && mx > now + kTRoom ? mx - kTRoom : now;
+            if (next != ref) sum *= ex2a(ref - next);
+            ref = next;
+            if ((c > 0 || h > 0) && __any_sync(0xffffffffu, next != now)) {
+              // O holds the keys before these, once their P V has landed
+              // (the chunk's before first: a parity names a phase only if the one before is complete)
+              ok = k == 0 || ver_wait_warp(s, &s.p_free[grp ^ 1], uint32_t((k - 1) >> 1) & 1, a.err);
+              if (ok && h == 1) ok = ver_wait_warp(s, &s.h_done, uint32_t(k) & 1, a.err);
               if (!ok) break;
               tc_fence_after();
+              const float al = next == now ? 1.f : ex2a(now - next);
 #pragma unroll 1
               for (int h2 = 0; h2 < D / 32; ++h2) {
                 float ov[32];
@@ -481,22 +502,33 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
             weigh();
           }
           sum += part;
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = pack_half2(x[2 * e], x[2 * e + 1]);
-          tmem_st32u(trow + kVerChunk * st + 32 * h, w);
+          tmem_st32u(trow + kVerChunk * grp + 32 * h, w);
+          if (h == 1) s.ref[m] = ref;
           tc_fence_before();
-          mbar_arrive(&s.p_full[2 * st + h]);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&s.p_full[2 * grp + h]);
+            if (h == 1) mbar_arrive(&s.decided[wp][grp]);
+          }
         }
       }
-      if (!ok || !twait_warp(s, &s.o_full, uint32_t(piece) & 1, a.err)) break;
+      if (!ok) break;
+      // both warps' sums of the row; the larger reference is O's
+      s.state[piece & 1][grp][m] = make_float2(sum, ref);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.joined[wp]);
+      if (!ver_wait_warp(s, &s.joined[wp], uint32_t(piece) & 1, a.err)) break;
+      const float2 other = s.state[piece & 1][grp ^ 1][m];
+      const float last = fmaxf(ref, other.y);
+      sum = (ref == last ? sum : sum * ex2a(ref - last)) + (other.y == last ? other.x : other.x * ex2a(other.y - last));
+      if (!ver_wait_warp(s, &s.o_full, uint32_t(piece) & 1, a.err)) break;
       tc_fence_after();
       const bool whole = p.c0 == 0 && p.c1 == p.n;
       const int64_t slot = ver_slot(blockIdx.x, p);
       const float inv = !whole ? 1.f : (sum != 0.f ? 1.f / sum : 0.f);
       const int64_t seen_keys = ver_limit(p, i) - p.c0 * kVerChunk;
 #pragma unroll 1
-      for (int h = 0; h < D / 32; ++h) {
+      for (int h = grp * (D / 64); h < (grp + 1) * (D / 64); ++h) {  // half of the columns each
         float o[32];
         tmem_ld32(trow + kTO + 32 * h, o);
         if (real) {
@@ -524,26 +556,27 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
           }
         }
       }
-      if (!whole && real) {
-        a.part_ml[(slot * a.MR + m) * 2] = ref;
+      if (!whole && real && grp == 0) {
+        a.part_ml[(slot * a.MR + m) * 2] = last;
         a.part_ml[(slot * a.MR + m) * 2 + 1] = sum;
       }
       tc_fence_before();
-      mbar_arrive(&s.o_free);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.o_free);
     }
   }
 
   __syncthreads();
-  if ((warp == 12 || warp == 13) && s.abort) {  // the MMAs issued so far, before TMEM is freed
+  if ((warp == kTQkWarp || warp == kTPvWarp) && s.abort) {  // the MMAs issued so far, before TMEM is freed
     if (elect_one()) {
-      mma_commit(&s.drain[warp - 12]);
-      mbar_wait_bounded(&s.drain[warp - 12], 0, kWaitLimit);
+      mma_commit(&s.drain[warp - kTQkWarp]);
+      mbar_wait_bounded(&s.drain[warp - kTQkWarp], 0, kWaitLimit);
     }
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kTQkWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTCols) : "memory");
   }
@@ -551,7 +584,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
 
 template <int D>
 cudaError_t launch_tc(const VerArgs& a, cudaStream_t stream) {
-  constexpr int smem = 4 * kVerChunk * D * 2 + 1024;
+  constexpr int smem = 4 * kVerChunk * D * 2 + kTRing * kVerChunk * (D + D / 8) + 1024;
   const cudaError_t e = cudaFuncSetAttribute(verify_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return ver_launch(verify_tc_kernel<D>, a.G, kTThreads, smem, stream, a);
