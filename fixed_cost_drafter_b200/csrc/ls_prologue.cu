@@ -315,26 +315,60 @@ prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtenso
       mbar_arrive(&s.epi);
       return __all_sync(0xffffffffu, pwait(s, &s.epi, uint32_t(meets++) & 1, a.err));
     };
-    // the adapters' part of this thread's weight row, activation rows col .. col + n - 1
+    // The adapters' part: v[j] += B[n] . low[row] for this thread's weight row n and activation
+    // rows col .. col + n - 1. On CUDA cores in fp32: it runs beside the next unit's products
+    // (two accumulators), which take longer up to a rank of about 64. A sequence's row of B is
+    // read once for its rows; low is the same address for the whole warp.
+    const int R = lora.bank.rank;
+    auto adapter_row = [&](const PUnit& u, const PProblem& P, int sq) -> const __nv_bfloat16* {
+      const int ad = lora.bank.adapter_of[sq];
+      if (ad < 0 || ad >= lora.bank.n_adapters) return nullptr;
+      return static_cast<const __nv_bfloat16*>(u.p ? lora.bank.b_kv : lora.bank.b_q) +
+             ((int64_t(ad) * a.L + u.l) * P.n_out + u.nt * kPTileN + ecol) * R;
+    };
+    auto dot8 = [](const float (&w)[8], const float* h, float x) -> float {
+      const float4 p = __ldg(reinterpret_cast<const float4*>(h)), q = __ldg(reinterpret_cast<const float4*>(h) + 1);
+      return fmaf(w[7], q.w, fmaf(w[6], q.z, fmaf(w[5], q.y, fmaf(w[4], q.x,
+             fmaf(w[3], p.w, fmaf(w[2], p.z, fmaf(w[1], p.y, fmaf(w[0], p.x, x))))))));
+    };
     auto add_low = [&](const PUnit& u, const PProblem& P, int col, int n, float (&v)[32]) {
-      const int R = lora.bank.rank;
+      const int rps = P.rows_per_seq, seq0 = u.mt * P.seq_per_unit;
+      const float* low = lora.low[u.p] + int64_t(u.l) * rps * R;
+      const int64_t seq_step = int64_t(a.L) * rps * R;
+      if (rps % 16 == 0) {  // whole 16-row halves belong to one sequence
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (j >= n) break;
-        const int m = col + j, sq = u.mt * P.seq_per_unit + m / P.rows_per_seq, r = m % P.rows_per_seq;
-        const int ad = lora.bank.adapter_of[sq];
-        if (ad < 0 || ad >= lora.bank.n_adapters) continue;
-        const float* h = lora.low[u.p] + ((int64_t(sq) * a.L + u.l) * P.rows_per_seq + r) * R;
-        const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(u.p ? lora.bank.b_kv : lora.bank.b_q) +
-                                 ((int64_t(ad) * a.L + u.l) * P.n_out + u.nt * kPTileN + ecol) * R;
-        float x = 0.f;
-        for (int e = 0; e < R; e += 8) {
-          float f[8];
-          Elem<__nv_bfloat16>::to_f32(ld_nc_v4(w + e), f);
+        for (int h = 0; h < 2; ++h) {
+          if (16 * h >= n) break;
+          const int m = col + 16 * h, sq = seq0 + m / rps;
+          const __nv_bfloat16* w = adapter_row(u, P, sq);
+          if (!w) continue;
+          const float* x = low + sq * seq_step + (m % rps) * R;
+          for (int e = 0; e < R; e += 8) {
+            float f[8];
+            Elem<__nv_bfloat16>::to_f32(ld_nc_v4(w + e), f);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) x = fmaf(f[q], h[e + q], x);
+            for (int j = 0; j < 16; ++j) v[16 * h + j] = dot8(f, x + j * R + e, v[16 * h + j]);
+          }
         }
-        v[j] += x;
+        return;
+      }
+      for (int e = 0; e < R; e += 8) {
+        int sq = seq0 + col / rps, r = col % rps;
+        const __nv_bfloat16* w = nullptr;
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j >= n) break;
+          if (j == 0 || r == 0) {
+            w = adapter_row(u, P, sq);
+            if (w) Elem<__nv_bfloat16>::to_f32(ld_nc_v4(w + e), f);
+          }
+          if (w) v[j] = dot8(f, low + sq * seq_step + r * R + e, v[j]);
+          if (++r == rps) {
+            r = 0;
+            ++sq;
+          }
+        }
       }
     };
     auto store_tile = [&](const PUnit& u, const PProblem& P, auto&& fetch) -> bool {
@@ -445,47 +479,86 @@ prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtenso
   }
 }
 
-// low[p][b][l][row][r] = scale (A x): a warp per r of a (sequence, layer), up to 16 rows at a time.
-__global__ void __launch_bounds__(256) lora_low_kernel(const PLora lora, const __nv_bfloat16* x,
-                                                       const __nv_bfloat16* boundary, int L, int B, int hidden,
-                                                       int32_t* err) {
-  const int b = int(blockIdx.x) / L, l = int(blockIdx.x) - b * L, p = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = lora.bank.rank;
-  const int rows = p ? 1 : B;
+// low[p][b][l][row][r] = scale (A x), a CTA per (sequence, layer), problem and 64 of the rank.
+// Its bytes (x and A once each) are few beside the weights'; what counts is the latency, so the
+// hidden size is spread over the CTA's warps, 32 entries at a time: a thread's 16-byte load of
+// eight entries of a row is its part of two m16n8k16 products' operands (their k order is free).
+// The warps' sums are added in warp order.
+constexpr int kLowWarps = 8;
+constexpr int kLowRank = 64;  // rank entries per CTA: 8 n-tiles
+
+__device__ inline void mma_bf16_warp(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// MT: 16-row tiles of activation rows (block rows up to 32).
+template <int MT>
+__global__ void __launch_bounds__(kLowWarps * 32) lora_low_kernel(const PLora lora, const __nv_bfloat16* x,
+                                                                  const __nv_bfloat16* boundary, int L, int B,
+                                                                  int hidden, int32_t* err) {
+  __shared__ __align__(16) float red[kLowWarps][16][kLowRank];
+  const int b = int(blockIdx.x) / L, l = int(blockIdx.x) - b * L, p = blockIdx.y, r0 = int(blockIdx.z) * kLowRank;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int R = lora.bank.rank, rows = p ? 1 : B, nr = min(kLowRank, R - r0);
+  grid_dependency_wait();
+  allow_dependent_launch();
   const int ad = lora.bank.adapter_of[b];
-  const bool none = ad < 0 || ad >= lora.bank.n_adapters;
-  if (none && ad != -1 && threadIdx.x == 0) set_err(err, LS_DEVERR_ADAPTER);
-  const __nv_bfloat16* src = p ? boundary + (int64_t(b) * L + l) * hidden : x + (int64_t(b) * L + l) * B * hidden;
-  float* low = lora.low[p] + (int64_t(b) * L + l) * rows * R;
-  const float scale = none ? 0.f : lora.bank.scale[ad];
-  for (int r = warp; r < R; r += 8) {
-    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p ? lora.bank.a_kv : lora.bank.a_q) +
-                             ((int64_t(none ? 0 : ad) * L + l) * R + r) * hidden;
-    for (int i0 = 0; i0 < rows; i0 += 16) {
-      float acc[16];
+  float* low = lora.low[p] + (int64_t(b) * L + l) * rows * R + r0;
+  if (ad < 0 || ad >= lora.bank.n_adapters) {  // none: zeros
+    if (ad != -1 && threadIdx.x == 0) set_err(err, LS_DEVERR_ADAPTER);
+    for (int i = threadIdx.x; i < rows * nr; i += kLowWarps * 32) low[(i / nr) * R + i % nr] = 0.f;
+    return;
+  }
+  const __nv_bfloat16* src = (p ? boundary : x) + (int64_t(b) * L + l) * rows * hidden + t * 8;
+  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p ? lora.bank.a_kv : lora.bank.a_q) +
+                           ((int64_t(ad) * L + l) * R + r0) * hidden + t * 8;
+  float acc[MT][kLowRank / 8][4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-      if (!none) {
-        for (int k = lane * 8; k < hidden; k += 256) {
-          float f[8];
-          Elem<__nv_bfloat16>::to_f32(ld_nc_v4(w + k), f);
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (i0 + i >= rows) break;
-            float g[8];
-            Elem<__nv_bfloat16>::to_f32(ld_nc_v4(src + int64_t(i0 + i) * hidden + k), g);
+    for (int n = 0; n < kLowRank / 8; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+  // (rows past the last are read as the last one again and not stored)
+  const __nv_bfloat16* xr[2 * MT];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[i] = fmaf(f[e], g[e], acc[i]);
-          }
-        }
+  for (int m = 0; m < 2 * MT; ++m) xr[m] = src + int64_t(min(m * 8 + g, rows - 1)) * hidden;
+  const __nv_bfloat16* wr = w + int64_t(g) * hidden;
+#pragma unroll 2
+  for (int k = warp * 32; k < hidden; k += kLowWarps * 32) {
+    uint4 av[2 * MT];
+#pragma unroll
+    for (int m = 0; m < 2 * MT; ++m) av[m] = ld_nc_v4(xr[m] + k);
+#pragma unroll
+    for (int n = 0; n < kLowRank / 8; ++n) {
+      if (8 * n >= nr) break;
+      const uint4 bv = ld_nc_v4(wr + int64_t(8 * n) * hidden + k);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        mma_bf16_warp(acc[m][n], av[2 * m].x, av[2 * m + 1].x, av[2 * m].y, av[2 * m + 1].y, bv.x, bv.y);
+        mma_bf16_warp(acc[m][n], av[2 * m].z, av[2 * m + 1].z, av[2 * m].w, av[2 * m + 1].w, bv.z, bv.w);
       }
+    }
+  }
+  const float scale = lora.bank.scale[ad];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (i0 + i >= rows) break;
+  for (int m = 0; m < MT; ++m) {
+    if (m > 0) __syncthreads();
 #pragma unroll
-        for (int o = 16; o; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-        if (lane == 0) low[int64_t(i0 + i) * R + r] = none ? 0.f : scale * acc[i];
-      }
+    for (int n = 0; n < kLowRank / 8; ++n) {
+      *reinterpret_cast<float2*>(&red[warp][g][8 * n + 2 * t]) = make_float2(acc[m][n][0], acc[m][n][1]);
+      *reinterpret_cast<float2*>(&red[warp][g + 8][8 * n + 2 * t]) = make_float2(acc[m][n][2], acc[m][n][3]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * nr; i += kLowWarps * 32) {
+      const int row = i / nr, r = i - row * nr;
+      if (16 * m + row >= rows) break;
+      float sum = 0.f;
+#pragma unroll
+      for (int v = 0; v < kLowWarps; ++v) sum += red[v][row][r];
+      low[(16 * m + row) * R + r] = scale * sum;
     }
   }
 }
@@ -575,10 +648,18 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
     pl.bank = *lora;
     pl.low[0] = static_cast<float*>(low);
     pl.low[1] = pl.low[0] + int64_t(p.b) * p.L * p.B * lora->rank;
-    lora_low_kernel<<<dim3(p.b * p.L, 2), 256, 0, stream>>>(pl, static_cast<const __nv_bfloat16*>(x),
-                                                            reinterpret_cast<const __nv_bfloat16*>(p.boundary), p.L,
-                                                            p.B, p.hidden, p.err);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(p.b * p.L, 2, (lora->rank + kLowRank - 1) / kLowRank);
+    lc.blockDim = dim3(kLowWarps * 32);
+    lc.stream = stream;
+    cudaLaunchAttribute la[1];
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = la;
+    lc.numAttrs = 1;
+    e = cudaLaunchKernelEx(&lc, p.B > 16 ? lora_low_kernel<2> : lora_low_kernel<1>, pl,
+                           static_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(p.boundary),
+                           p.L, p.B, p.hidden, p.err);
     if (e != cudaSuccess) return e;
   }
   int grid = sms < kProMaxGrid ? sms : kProMaxGrid;
