@@ -75,11 +75,16 @@ struct PArgs {
   int32_t* err;
 };
 
-// Low-rank adapters (ls_draft_prologue_lora): low[p] holds scale * (A x) of problem p in fp32,
-// [b][L][rows_per_seq][rank], 0 for a sequence without an adapter.
+// Low-rank adapters (ls_draft_prologue_lora): scale * (A x) of problem p, by lora_low_kernel.
+// Block queries whose blocks are whole 16-row steps of the MMA's N take them as further k-steps
+// of their unit: weight rows B_a of the sequence's adapter against split[], low as two bf16
+// parts (high + low: 16 bits of the fp32 sum), into the sequence's accumulator columns only. The
+// others (boundary rows, whose sequences share 16 columns; odd blocks) are added by the epilogue
+// in fp32 from low[p], so that no adapter's infinities reach another sequence.
 struct PLora {
   ls_lora bank;
-  float* low[2];
+  float* low[2];         // [b][L][rows_per_seq][rank]
+  __nv_bfloat16* split;  // [b][L][2][B][rank], null: low[0] is used
 };
 
 struct PBars {
@@ -179,8 +184,9 @@ __device__ inline bool pwait(PBars& s, uint64_t* bar, uint32_t parity, int32_t* 
 
 template <bool kLora>
 __global__ void __launch_bounds__(kPThreads, 1)
-prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtensorMap w0, const __grid_constant__ CUtensorMap x0,
-                const __grid_constant__ CUtensorMap w1, const __grid_constant__ CUtensorMap x1) {
+prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora lora, const __grid_constant__ CUtensorMap w0, const __grid_constant__ CUtensorMap x0,
+                const __grid_constant__ CUtensorMap w1, const __grid_constant__ CUtensorMap x1,
+                const __grid_constant__ CUtensorMap wl, const __grid_constant__ CUtensorMap xl) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ PBars s;
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -217,6 +223,23 @@ prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtenso
     allow_dependent_launch();
   }
 
+  // The sequences of a unit that take further k-steps for their adapters: calls
+  // step(sequence of the tile, adapter, rank chunk of 64) in order until it returns false.
+  auto adapter_steps = [&](const PItem& it, const PUnit& u, auto&& step) -> bool {
+    if constexpr (kLora) {
+      if (u.p != 0 || !lora.split || it.k1 != a.k_steps) return true;
+      const PProblem& P = a.pr[0];
+      const int seq0 = u.mt * P.seq_per_unit, n = min(P.seq_per_unit, a.b - seq0);
+      for (int i = 0; i < n; ++i) {
+        const int ad = lora.bank.adapter_of[seq0 + i];
+        if (ad < 0 || ad >= lora.bank.n_adapters) continue;
+        for (int rc = 0; rc < lora.bank.rank; rc += kPKStep)
+          if (!step(i, ad, rc)) return false;
+      }
+    }
+    return true;
+  };
+
   if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ TMA producers
     // warp 0: the weights (A) of every k-step; warp 6: the activations (B)
@@ -237,9 +260,8 @@ prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtenso
         const uint32_t bytes = is_a ? uint32_t(kPABytes) : uint32_t(P.load_rows * kPKStep * 2);
         // the weights are read once: they must not push the activations (read again by
         // every weight tile of the layer) out of L2
-        for (int ks = it.k0; ks < it.k1; ++ks, ++k) {
-          const int st = k % nst;          // this ring's stage
-          uint64_t* full = &s.afull[k % kPAStages];  // the k-step's barrier
+        // k-step k's stage of this ring is free for its next copy (false: gave up)
+        auto begin_step = [&](uint32_t n_bytes) -> bool {
           if (k == nst && !waited) {  // (the first ring's weights are in flight)
             grid_dependency_wait();
             allow_dependent_launch();
@@ -249,11 +271,14 @@ prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtenso
           // (k - nst); the MMAs of a k-step complete in order, and the one wait before for
           // the same barrier covered its previous phase, so the parity names this phase
           const int prev = k - nst;
-          if (prev >= 0 && !pwait(s, &s.aempty[prev % kPAStages], uint32_t(prev / kPAStages) & 1, a.err)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(full, bytes);
+          if (prev >= 0 && !pwait(s, &s.aempty[prev % kPAStages], uint32_t(prev / kPAStages) & 1, a.err)) return false;
+          mbar_arrive_expect_tx(&s.afull[k % kPAStages], n_bytes);
+          return true;
+        };
+        for (int ks = it.k0; ks < it.k1; ++ks, ++k) {
+          const int st = k % nst;                    // this ring's stage
+          uint64_t* full = &s.afull[k % kPAStages];  // the k-step's barrier
+          if (!begin_step(bytes)) { ok = false; break; }
           if (is_a)
             tma_load_2d_hint(a_ring + st * kPABytes, m, ks * kPKStep, u.l * P.n_out + u.nt * kPTileN, full, pol);
           else if (P.is_4d)
@@ -261,6 +286,24 @@ prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtenso
           else
             tma_load_3d_hint(b_ring + st * kPBBytes, m, ks * kPKStep, u.l, u.mt * P.seq_per_unit, full, pol);
         }
+        if (!ok) break;
+        if (kLora && !waited) {  // the adapters' ids and inner products are the kernel before's
+          grid_dependency_wait();
+          allow_dependent_launch();
+          waited = true;
+        }
+        ok = adapter_steps(it, u, [&](int i, int ad, int rc) -> bool {
+          const int st = k % nst;
+          uint64_t* full = &s.afull[k % kPAStages];
+          if (!begin_step(is_a ? uint32_t(kPABytes) : uint32_t(2 * P.rows_per_seq * kPKStep * 2))) return false;
+          if (is_a)
+            tma_load_2d(a_ring + st * kPABytes, &wl, rc, (ad * a.L + u.l) * P.n_out + u.nt * kPTileN, full);
+          else
+            tma_load_2d(b_ring + st * kPBBytes, &xl, rc,
+                        ((u.mt * P.seq_per_unit + i) * a.L + u.l) * 2 * P.rows_per_seq, full);
+          ++k;
+          return true;
+        });
       }
       s.issued[is_a ? 0 : 1] = k;
     }
@@ -293,6 +336,22 @@ prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtenso
             mma_bf16(d, da + uint32_t(kk * 2), db + uint32_t(kk * 2), id, (ks > it.k0 || kk > 0) ? 1u : 0u);
           mma_commit(&s.aempty[sa]);  // frees both stages of the k-step
         }
+        if (ok)
+          ok = adapter_steps(it, u, [&](int i, int, int rc) -> bool {
+            const int sa = k % kPAStages, sb = k % kPBStages;
+            if (!pwait(s, &s.afull[sa], (k / kPAStages) & 1, a.err)) return false;
+            tc_fence_after();
+            const uint64_t da = sdesc(smem_u32(a_ring + sa * kPABytes), 16, 1024);
+            const uint64_t db = sdesc(smem_u32(b_ring + sb * kPBBytes), 16, 1024);
+            const uint32_t ids = idesc_bf16(P.rows_per_seq, false, kPTileN), ds = d + uint32_t(i * P.rows_per_seq);
+            for (int part = 0; part < 2; ++part)  // the high and the low part of the inner products
+              for (int kk = 0; kk < kPKStep / 16 && rc + 16 * kk < lora.bank.rank; ++kk)
+                mma_bf16(ds, da + uint32_t(kk * 2),
+                         db + uint32_t((part * P.rows_per_seq * kPKStep * 2 >> 4) + kk * 2), ids, 1u);
+            mma_commit(&s.aempty[sa]);
+            ++k;
+            return true;
+          });
         if (ok) mma_commit(&s.acc_full[ab]);
       }
     }
@@ -315,60 +374,49 @@ prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtenso
       mbar_arrive(&s.epi);
       return __all_sync(0xffffffffu, pwait(s, &s.epi, uint32_t(meets++) & 1, a.err));
     };
-    // The adapters' part: v[j] += B[n] . low[row] for this thread's weight row n and activation
-    // rows col .. col + n - 1. On CUDA cores in fp32: it runs beside the next unit's products
-    // (two accumulators), which take longer up to a rank of about 64. A sequence's row of B is
-    // read once for its rows; low is the same address for the whole warp.
+    // The adapters' part where no further k-steps bring it: v[j] += B[n] . low[row] for this
+    // thread's weight row n and activation rows col .. col + n - 1, in fp32 on CUDA cores, beside
+    // the next unit's products. Eight rows' loads are in flight together (a sequence without an
+    // adapter reads adapter 0 and leaves its sum out); low is one address for the whole warp.
     const int R = lora.bank.rank;
-    auto adapter_row = [&](const PUnit& u, const PProblem& P, int sq) -> const __nv_bfloat16* {
-      const int ad = lora.bank.adapter_of[sq];
-      if (ad < 0 || ad >= lora.bank.n_adapters) return nullptr;
-      return static_cast<const __nv_bfloat16*>(u.p ? lora.bank.b_kv : lora.bank.b_q) +
-             ((int64_t(ad) * a.L + u.l) * P.n_out + u.nt * kPTileN + ecol) * R;
-    };
-    auto dot8 = [](const float (&w)[8], const float* h, float x) -> float {
-      const float4 p = __ldg(reinterpret_cast<const float4*>(h)), q = __ldg(reinterpret_cast<const float4*>(h) + 1);
-      return fmaf(w[7], q.w, fmaf(w[6], q.z, fmaf(w[5], q.y, fmaf(w[4], q.x,
-             fmaf(w[3], p.w, fmaf(w[2], p.z, fmaf(w[1], p.y, fmaf(w[0], p.x, x))))))));
-    };
     auto add_low = [&](const PUnit& u, const PProblem& P, int col, int n, float (&v)[32]) {
       const int rps = P.rows_per_seq, seq0 = u.mt * P.seq_per_unit;
-      const float* low = lora.low[u.p] + int64_t(u.l) * rps * R;
-      const int64_t seq_step = int64_t(a.L) * rps * R;
-      if (rps % 16 == 0) {  // whole 16-row halves belong to one sequence
+      const __nv_bfloat16* bank = static_cast<const __nv_bfloat16*>(u.p ? lora.bank.b_kv : lora.bank.b_q) +
+                                  (int64_t(u.l) * P.n_out + u.nt * kPTileN + ecol) * R;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (16 * h >= n) break;
-          const int m = col + 16 * h, sq = seq0 + m / rps;
-          const __nv_bfloat16* w = adapter_row(u, P, sq);
-          if (!w) continue;
-          const float* x = low + sq * seq_step + (m % rps) * R;
-          for (int e = 0; e < R; e += 8) {
+      for (int j0 = 0; j0 < 32; j0 += 8) {
+        if (j0 >= n) break;
+        const __nv_bfloat16* w[8];
+        const float* h[8];
+        float x[8];
+        uint32_t has = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int m = col + min(j0 + j, n - 1), sq = seq0 + m / rps;
+          const int ad = lora.bank.adapter_of[sq];
+          const bool one = ad >= 0 && ad < lora.bank.n_adapters;
+          has |= uint32_t(one) << j;
+          w[j] = bank + int64_t(one ? ad : 0) * a.L * P.n_out * R;
+          h[j] = lora.low[u.p] + ((int64_t(sq) * a.L + u.l) * rps + m % rps) * R;
+          x[j] = 0.f;
+        }
+#pragma unroll 1
+        for (int e = 0; e < R; e += 8) {
+          uint4 wv[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) wv[j] = ld_nc_v4(w[j] + e);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
             float f[8];
-            Elem<__nv_bfloat16>::to_f32(ld_nc_v4(w + e), f);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[16 * h + j] = dot8(f, x + j * R + e, v[16 * h + j]);
+            Elem<__nv_bfloat16>::to_f32(wv[j], f);
+            const float4 p = __ldg(reinterpret_cast<const float4*>(h[j] + e)), q = __ldg(reinterpret_cast<const float4*>(h[j] + e) + 1);
+            x[j] += fmaf(f[3], p.w, fmaf(f[2], p.z, fmaf(f[1], p.y, f[0] * p.x))) +
+                    fmaf(f[7], q.w, fmaf(f[6], q.z, fmaf(f[5], q.y, f[4] * q.x)));
           }
         }
-        return;
-      }
-      for (int e = 0; e < R; e += 8) {
-        int sq = seq0 + col / rps, r = col % rps;
-        const __nv_bfloat16* w = nullptr;
-        float f[8];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j >= n) break;
-          if (j == 0 || r == 0) {
-            w = adapter_row(u, P, sq);
-            if (w) Elem<__nv_bfloat16>::to_f32(ld_nc_v4(w + e), f);
-          }
-          if (w) v[j] = dot8(f, low + sq * seq_step + r * R + e, v[j]);
-          if (++r == rps) {
-            r = 0;
-            ++sq;
-          }
-        }
+        for (int j = 0; j < 8; ++j)
+          if ((has >> j) & 1) v[j0 + j] += x[j];
       }
     };
     auto store_tile = [&](const PUnit& u, const PProblem& P, auto&& fetch) -> bool {
@@ -381,7 +429,9 @@ prologue_kernel(const PArgs a, const PLora lora, const __grid_constant__ CUtenso
         for (int c0 = 0; c0 < nr; c0 += 32) {
           float v[32];
           fetch(r0 + c0, v);
-          if constexpr (kLora) add_low(u, P, r0 + c0, min(32, rows - r0 - c0), v);
+          if constexpr (kLora) {
+            if ((u.p || !lora.split) && r0 + c0 < rows) add_low(u, P, r0 + c0, min(32, rows - r0 - c0), v);
+          }
 #pragma unroll
           for (int j = 0; j < 32; ++j) stage[(c0 + j) * kPTileN + ecol] = __float2bfloat16_rn(v[j]);
         }
@@ -495,9 +545,11 @@ __device__ inline void mma_bf16_warp(float (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// MT: 16-row tiles of activation rows (block rows up to 32).
-template <int MT>
-__global__ void __launch_bounds__(kLowWarps * 32) lora_low_kernel(const PLora lora, const __nv_bfloat16* x,
+// MT: 16-row tiles of activation rows (block rows up to 32). NT: 8-entry tiles of the rank (rank
+// entries past the last are read as the last one again and not stored: with a branch per tile
+// the loads would wait for one another).
+template <int MT, int NT>
+__global__ void __launch_bounds__(kLowWarps * 32) lora_low_kernel(const __grid_constant__ PLora lora, const __nv_bfloat16* x,
                                                                   const __nv_bfloat16* boundary, int L, int B,
                                                                   int hidden, int32_t* err) {
   __shared__ __align__(16) float red[kLowWarps][16][kLowRank];
@@ -508,46 +560,48 @@ __global__ void __launch_bounds__(kLowWarps * 32) lora_low_kernel(const PLora lo
   allow_dependent_launch();
   const int ad = lora.bank.adapter_of[b];
   float* low = lora.low[p] + (int64_t(b) * L + l) * rows * R + r0;
-  if (ad < 0 || ad >= lora.bank.n_adapters) {  // none: zeros
+  __nv_bfloat16* split = p == 0 && lora.split ? lora.split + (int64_t(b) * L + l) * 2 * B * R + r0 : nullptr;
+  if (ad < 0 || ad >= lora.bank.n_adapters) {  // none: nothing of it is read with a meaning (zeros: finite)
     if (ad != -1 && threadIdx.x == 0) set_err(err, LS_DEVERR_ADAPTER);
-    for (int i = threadIdx.x; i < rows * nr; i += kLowWarps * 32) low[(i / nr) * R + i % nr] = 0.f;
+    if (!split)
+      for (int i = threadIdx.x; i < rows * nr; i += kLowWarps * 32) low[(i / nr) * R + i % nr] = 0.f;
     return;
   }
   const __nv_bfloat16* src = (p ? boundary : x) + (int64_t(b) * L + l) * rows * hidden + t * 8;
   const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p ? lora.bank.a_kv : lora.bank.a_q) +
                            ((int64_t(ad) * L + l) * R + r0) * hidden + t * 8;
-  float acc[MT][kLowRank / 8][4];
+  float acc[MT][NT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < kLowRank / 8; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+    for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
   // (rows past the last are read as the last one again and not stored)
-  const __nv_bfloat16* xr[2 * MT];
+  const __nv_bfloat16 *xr[2 * MT], *wr[NT];
 #pragma unroll
   for (int m = 0; m < 2 * MT; ++m) xr[m] = src + int64_t(min(m * 8 + g, rows - 1)) * hidden;
-  const __nv_bfloat16* wr = w + int64_t(g) * hidden;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) wr[n] = w + int64_t(min(8 * n + g, nr - 1)) * hidden;
 #pragma unroll 2
   for (int k = warp * 32; k < hidden; k += kLowWarps * 32) {
-    uint4 av[2 * MT];
+    uint4 av[2 * MT], bv[NT];
 #pragma unroll
     for (int m = 0; m < 2 * MT; ++m) av[m] = ld_nc_v4(xr[m] + k);
 #pragma unroll
-    for (int n = 0; n < kLowRank / 8; ++n) {
-      if (8 * n >= nr) break;
-      const uint4 bv = ld_nc_v4(wr + int64_t(8 * n) * hidden + k);
+    for (int n = 0; n < NT; ++n) bv[n] = ld_nc_v4(wr[n] + k);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        mma_bf16_warp(acc[m][n], av[2 * m].x, av[2 * m + 1].x, av[2 * m].y, av[2 * m + 1].y, bv.x, bv.y);
-        mma_bf16_warp(acc[m][n], av[2 * m].z, av[2 * m + 1].z, av[2 * m].w, av[2 * m + 1].w, bv.z, bv.w);
+        mma_bf16_warp(acc[m][n], av[2 * m].x, av[2 * m + 1].x, av[2 * m].y, av[2 * m + 1].y, bv[n].x, bv[n].y);
+        mma_bf16_warp(acc[m][n], av[2 * m].z, av[2 * m + 1].z, av[2 * m].w, av[2 * m + 1].w, bv[n].z, bv[n].w);
       }
-    }
   }
   const float scale = lora.bank.scale[ad];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     if (m > 0) __syncthreads();
 #pragma unroll
-    for (int n = 0; n < kLowRank / 8; ++n) {
+    for (int n = 0; n < NT; ++n) {
       *reinterpret_cast<float2*>(&red[warp][g][8 * n + 2 * t]) = make_float2(acc[m][n][0], acc[m][n][1]);
       *reinterpret_cast<float2*>(&red[warp][g + 8][8 * n + 2 * t]) = make_float2(acc[m][n][2], acc[m][n][3]);
     }
@@ -558,7 +612,15 @@ __global__ void __launch_bounds__(kLowWarps * 32) lora_low_kernel(const PLora lo
       float sum = 0.f;
 #pragma unroll
       for (int v = 0; v < kLowWarps; ++v) sum += red[v][row][r];
-      low[(16 * m + row) * R + r] = scale * sum;
+      sum *= scale;
+      if (split) {
+        const __nv_bfloat16 hi = __float2bfloat16_rn(sum);
+        const float rest = sum - __bfloat162float(hi);
+        split[(16 * m + row) * R + r] = hi;
+        split[(B + 16 * m + row) * R + r] = __float2bfloat16_rn(fabsf(rest) <= 3e38f ? rest : 0.f);
+      } else {
+        low[(16 * m + row) * R + r] = sum;
+      }
     }
   }
 }
@@ -644,10 +706,23 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
     if (!encode_bf16(p.boundary, 3, dims, str, box, &mx1)) return cudaErrorInvalidValue;
   }
   PLora pl{};
+  CUtensorMap mwl = mw0, mxl = mx0;  // (unused without adapters)
   if (lora) {
     pl.bank = *lora;
     pl.low[0] = static_cast<float*>(low);
     pl.low[1] = pl.low[0] + int64_t(p.b) * p.L * p.B * lora->rank;
+    if (p.B % 16 == 0) {
+      // the tiles' inner extent is 64 of the rank; what lies past it reads as zeros
+      pl.split = static_cast<__nv_bfloat16*>(low);  // (two bf16 parts in the place of fp32 sums)
+      const cuuint64_t rb = cuuint64_t(lora->rank) * 2;
+      const int64_t w_rows = int64_t(lora->n_adapters) * p.L * Q.n_out, x_rows = int64_t(p.b) * p.L * 2 * p.B;
+      if (w_rows > INT32_MAX || x_rows > INT32_MAX) return cudaErrorNotSupported;
+      const cuuint64_t wd[2] = {cuuint64_t(lora->rank), cuuint64_t(w_rows)}, xd[2] = {cuuint64_t(lora->rank), cuuint64_t(x_rows)};
+      const cuuint64_t str[1] = {rb};
+      const cuuint32_t wbox[2] = {kPKStep, kPTileN}, xbox[2] = {kPKStep, cuuint32_t(2 * p.B)};
+      if (!encode_bf16(const_cast<void*>(lora->b_q), 2, wd, str, wbox, &mwl)) return cudaErrorInvalidValue;
+      if (!encode_bf16(low, 2, xd, str, xbox, &mxl)) return cudaErrorInvalidValue;
+    }
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(p.b * p.L, 2, (lora->rank + kLowRank - 1) / kLowRank);
     lc.blockDim = dim3(kLowWarps * 32);
@@ -657,7 +732,11 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
     la[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = la;
     lc.numAttrs = 1;
-    e = cudaLaunchKernelEx(&lc, p.B > 16 ? lora_low_kernel<2> : lora_low_kernel<1>, pl,
+    const bool two = p.B > 16;
+    const auto low_kernel = lora->rank <= 16   ? (two ? lora_low_kernel<2, 2> : lora_low_kernel<1, 2>)
+                            : lora->rank <= 32 ? (two ? lora_low_kernel<2, 4> : lora_low_kernel<1, 4>)
+                                               : (two ? lora_low_kernel<2, 8> : lora_low_kernel<1, 8>);
+    e = cudaLaunchKernelEx(&lc, low_kernel, pl,
                            static_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(p.boundary),
                            p.L, p.B, p.hidden, p.err);
     if (e != cudaSuccess) return e;
@@ -687,7 +766,7 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, pl, mw0, mx0, mw1, mx1);
+  return cudaLaunchKernelEx(&cfg, kernel, a, pl, mw0, mx0, mw1, mx1, mwl, mxl);
 }
 
 }  // namespace ls
