@@ -529,13 +529,14 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
   }
 }
 
-// low[p][b][l][row][r] = scale (A x), a CTA per (sequence, layer), problem and 64 of the rank.
-// Its bytes (x and A once each) are few beside the weights'; what counts is the latency, so the
-// hidden size is spread over the CTA's warps, 32 entries at a time: a thread's 16-byte load of
-// eight entries of a row is its part of two m16n8k16 products' operands (their k order is free).
-// The warps' sums are added in warp order.
-constexpr int kLowWarps = 8;
-constexpr int kLowRank = 64;  // rank entries per CTA: 8 n-tiles
+// low[p][b][l][row][r] = scale (A x), a CTA per (sequence, layer), problem and 8 NT of the rank.
+// Its bytes (x and A once each) are few beside the weights'; what counts is the latency, as the
+// projections' kernel follows: 16 warps spread over the hidden size, 32 entries at a time (a
+// thread's 16-byte load of eight entries of a row is its part of two m16n8k16 products' operands,
+// their k order is free), with the loads of several steps in flight at once. The warps' sums are
+// added in warp order. (Run beside the projections instead, a warp per 8 of the rank and no shared
+// memory, it took longer than their first units: 160 us instead of 82 for 16 requests at rank 16.)
+constexpr int kLowWarps = 16;
 
 __device__ inline void mma_bf16_warp(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1) {
@@ -545,26 +546,24 @@ __device__ inline void mma_bf16_warp(float (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// MT: 16-row tiles of activation rows (block rows up to 32). NT: 8-entry tiles of the rank (rank
-// entries past the last are read as the last one again and not stored: with a branch per tile
-// the loads would wait for one another).
+// MT: 16-row tiles of activation rows (block rows up to 32). NT: 8-entry tiles of the rank. (Rows
+// and rank entries past the last are read as the last one again and not stored: with a branch
+// per tile the loads would wait for one another.)
 template <int MT, int NT>
 __global__ void __launch_bounds__(kLowWarps * 32) lora_low_kernel(const __grid_constant__ PLora lora, const __nv_bfloat16* x,
                                                                   const __nv_bfloat16* boundary, int L, int B,
                                                                   int hidden, int32_t* err) {
-  __shared__ __align__(16) float red[kLowWarps][16][kLowRank];
-  const int b = int(blockIdx.x) / L, l = int(blockIdx.x) - b * L, p = blockIdx.y, r0 = int(blockIdx.z) * kLowRank;
+  __shared__ __align__(16) float red[kLowWarps][16][8 * NT + 2];
+  const int b = int(blockIdx.x) / L, l = int(blockIdx.x) - b * L, p = blockIdx.y, r0 = int(blockIdx.z) * 8 * NT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int R = lora.bank.rank, rows = p ? 1 : B, nr = min(kLowRank, R - r0);
+  const int R = lora.bank.rank, rows = p ? 1 : B, nr = min(8 * NT, R - r0);
   grid_dependency_wait();
   allow_dependent_launch();
   const int ad = lora.bank.adapter_of[b];
   float* low = lora.low[p] + (int64_t(b) * L + l) * rows * R + r0;
   __nv_bfloat16* split = p == 0 && lora.split ? lora.split + (int64_t(b) * L + l) * 2 * B * R + r0 : nullptr;
-  if (ad < 0 || ad >= lora.bank.n_adapters) {  // none: nothing of it is read with a meaning (zeros: finite)
+  if (ad < 0 || ad >= lora.bank.n_adapters) {  // none: its place is read by the epilogue and left out
     if (ad != -1 && threadIdx.x == 0) set_err(err, LS_DEVERR_ADAPTER);
-    if (!split)
-      for (int i = threadIdx.x; i < rows * nr; i += kLowWarps * 32) low[(i / nr) * R + i % nr] = 0.f;
     return;
   }
   const __nv_bfloat16* src = (p ? boundary : x) + (int64_t(b) * L + l) * rows * hidden + t * 8;
@@ -575,26 +574,33 @@ __global__ void __launch_bounds__(kLowWarps * 32) lora_low_kernel(const __grid_c
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-  // (rows past the last are read as the last one again and not stored)
   const __nv_bfloat16 *xr[2 * MT], *wr[NT];
 #pragma unroll
   for (int m = 0; m < 2 * MT; ++m) xr[m] = src + int64_t(min(m * 8 + g, rows - 1)) * hidden;
 #pragma unroll
   for (int n = 0; n < NT; ++n) wr[n] = w + int64_t(min(8 * n + g, nr - 1)) * hidden;
-#pragma unroll 2
-  for (int k = warp * 32; k < hidden; k += kLowWarps * 32) {
-    uint4 av[2 * MT], bv[NT];
+  constexpr int kAhead = 2 * MT + NT <= 4 ? 4 : 2;  // steps whose loads are in flight together
+  for (int k0 = warp * 32; k0 < hidden; k0 += 32 * kLowWarps * kAhead) {
+    uint4 av[kAhead][2 * MT], bv[kAhead][NT];
 #pragma unroll
-    for (int m = 0; m < 2 * MT; ++m) av[m] = ld_nc_v4(xr[m] + k);
+    for (int s = 0; s < kAhead; ++s) {
+      const int k = min(k0 + 32 * kLowWarps * s, hidden - 32);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) bv[n] = ld_nc_v4(wr[n] + k);
+      for (int m = 0; m < 2 * MT; ++m) av[s][m] = ld_nc_v4(xr[m] + k);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) bv[s][n] = ld_nc_v4(wr[n] + k);
+    }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        mma_bf16_warp(acc[m][n], av[2 * m].x, av[2 * m + 1].x, av[2 * m].y, av[2 * m + 1].y, bv[n].x, bv[n].y);
-        mma_bf16_warp(acc[m][n], av[2 * m].z, av[2 * m + 1].z, av[2 * m].w, av[2 * m + 1].w, bv[n].z, bv[n].w);
-      }
+    for (int s = 0; s < kAhead; ++s) {
+      if (k0 + 32 * kLowWarps * s >= hidden) break;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          mma_bf16_warp(acc[m][n], av[s][2 * m].x, av[s][2 * m + 1].x, av[s][2 * m].y, av[s][2 * m + 1].y, bv[s][n].x, bv[s][n].y);
+          mma_bf16_warp(acc[m][n], av[s][2 * m].z, av[s][2 * m + 1].z, av[s][2 * m].w, av[s][2 * m + 1].w, bv[s][n].z, bv[s][n].w);
+        }
+    }
   }
   const float scale = lora.bank.scale[ad];
 #pragma unroll
@@ -617,7 +623,7 @@ __global__ void __launch_bounds__(kLowWarps * 32) lora_low_kernel(const __grid_c
         const __nv_bfloat16 hi = __float2bfloat16_rn(sum);
         const float rest = sum - __bfloat162float(hi);
         split[(16 * m + row) * R + r] = hi;
-        split[(B + 16 * m + row) * R + r] = __float2bfloat16_rn(fabsf(rest) <= 3e38f ? rest : 0.f);
+        split[(B + 16 * m + row) * R + r] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.f);  // (an infinite sum stays infinite)
       } else {
         low[(16 * m + row) * R + r] = sum;
       }
@@ -724,7 +730,8 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
       if (!encode_bf16(low, 2, xd, str, xbox, &mxl)) return cudaErrorInvalidValue;
     }
     cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(p.b * p.L, 2, (lora->rank + kLowRank - 1) / kLowRank);
+    const int tiles = lora->rank <= 8 ? 1 : (lora->rank <= 16 ? 2 : 4);  // (x is read again for each 32 of the rank)
+    lc.gridDim = dim3(p.b * p.L, 2, (lora->rank + 8 * tiles - 1) / (8 * tiles));
     lc.blockDim = dim3(kLowWarps * 32);
     lc.stream = stream;
     cudaLaunchAttribute la[1];
@@ -733,9 +740,9 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
     lc.attrs = la;
     lc.numAttrs = 1;
     const bool two = p.B > 16;
-    const auto low_kernel = lora->rank <= 16   ? (two ? lora_low_kernel<2, 2> : lora_low_kernel<1, 2>)
-                            : lora->rank <= 32 ? (two ? lora_low_kernel<2, 4> : lora_low_kernel<1, 4>)
-                                               : (two ? lora_low_kernel<2, 8> : lora_low_kernel<1, 8>);
+    const auto low_kernel = tiles == 1   ? (two ? lora_low_kernel<2, 1> : lora_low_kernel<1, 1>)
+                            : tiles == 2 ? (two ? lora_low_kernel<2, 2> : lora_low_kernel<1, 2>)
+                                         : (two ? lora_low_kernel<2, 4> : lora_low_kernel<1, 4>);
     e = cudaLaunchKernelEx(&lc, low_kernel, pl,
                            static_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(p.boundary),
                            p.L, p.B, p.hidden, p.err);
