@@ -79,12 +79,14 @@ struct PArgs {
 // Block queries whose blocks are whole 16-row steps of the MMA's N take them as further k-steps
 // of their unit: weight rows B_a of the sequence's adapter against split[], low as two bf16
 // parts (high + low: 16 bits of the fp32 sum), into the sequence's accumulator columns only. The
-// others (boundary rows, whose sequences share 16 columns; odd blocks) are added by the epilogue
-// in fp32 from low[p], so that no adapter's infinities reach another sequence.
+// others are added by the epilogue in fp32, so that no adapter's infinities reach another
+// sequence: odd blocks from low, boundary rows (whose sequences share 16 columns; one row is
+// cheap) as lora_low_kernel has multiplied them by B already.
 struct PLora {
   ls_lora bank;
-  float* low[2];         // [b][L][rows_per_seq][rank]
-  __nv_bfloat16* split;  // [b][L][2][B][rank], null: low[0] is used
+  float* low;            // [b][L][B][rank], or
+  __nv_bfloat16* split;  // [b][L][2][B][rank], null: low is used
+  float* add;            // [b][L][2 Hkv D]: scale * B (A boundary)
 };
 
 struct PBars {
@@ -344,10 +346,14 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
             const uint64_t da = sdesc(smem_u32(a_ring + sa * kPABytes), 16, 1024);
             const uint64_t db = sdesc(smem_u32(b_ring + sb * kPBBytes), 16, 1024);
             const uint32_t ids = idesc_bf16(P.rows_per_seq, false, kPTileN), ds = d + uint32_t(i * P.rows_per_seq);
-            for (int part = 0; part < 2; ++part)  // the high and the low part of the inner products
-              for (int kk = 0; kk < kPKStep / 16 && rc + 16 * kk < lora.bank.rank; ++kk)
-                mma_bf16(ds, da + uint32_t(kk * 2),
-                         db + uint32_t((part * P.rows_per_seq * kPKStep * 2 >> 4) + kk * 2), ids, 1u);
+            const uint32_t low_part = uint32_t(P.rows_per_seq * kPKStep * 2 >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kPKStep / 16; ++kk) {
+              if (rc + 16 * kk >= lora.bank.rank) break;
+#pragma unroll
+              for (int part = 0; part < 2; ++part)  // the high and the low part of the inner products
+                mma_bf16(ds, da + uint32_t(kk * 2), db + part * low_part + uint32_t(kk * 2), ids, 1u);
+            }
             mma_commit(&s.aempty[sa]);
             ++k;
             return true;
@@ -374,14 +380,25 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
       mbar_arrive(&s.epi);
       return __all_sync(0xffffffffu, pwait(s, &s.epi, uint32_t(meets++) & 1, a.err));
     };
-    // The adapters' part where no further k-steps bring it: v[j] += B[n] . low[row] for this
-    // thread's weight row n and activation rows col .. col + n - 1, in fp32 on CUDA cores, beside
-    // the next unit's products. Eight rows' loads are in flight together (a sequence without an
-    // adapter reads adapter 0 and leaves its sum out); low is one address for the whole warp.
+    // The adapters' part where no further k-steps bring it, for this thread's weight row n and
+    // activation rows col .. col + n - 1: boundary rows have theirs ready, odd blocks get
+    // B[n] . low[row], in fp32 on CUDA cores, beside the next unit's products. Eight rows' loads are
+    // in flight together (a sequence without an adapter reads adapter 0 and leaves its sum out);
+    // low is one address for the whole warp.
     const int R = lora.bank.rank;
     auto add_low = [&](const PUnit& u, const PProblem& P, int col, int n, float (&v)[32]) {
       const int rps = P.rows_per_seq, seq0 = u.mt * P.seq_per_unit;
-      const __nv_bfloat16* bank = static_cast<const __nv_bfloat16*>(u.p ? lora.bank.b_kv : lora.bank.b_q) +
+      if (u.p) {
+        const float* add = lora.add + (int64_t(seq0 + col) * a.L + u.l) * P.n_out + u.nt * kPTileN + ecol;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j >= n) break;
+          const int ad = lora.bank.adapter_of[seq0 + col + j];
+          if (ad >= 0 && ad < lora.bank.n_adapters) v[j] += __ldcg(add + int64_t(j) * a.L * P.n_out);
+        }
+        return;
+      }
+      const __nv_bfloat16* bank = static_cast<const __nv_bfloat16*>(lora.bank.b_q) +
                                   (int64_t(u.l) * P.n_out + u.nt * kPTileN + ecol) * R;
 #pragma unroll
       for (int j0 = 0; j0 < 32; j0 += 8) {
@@ -397,7 +414,7 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
           const bool one = ad >= 0 && ad < lora.bank.n_adapters;
           has |= uint32_t(one) << j;
           w[j] = bank + int64_t(one ? ad : 0) * a.L * P.n_out * R;
-          h[j] = lora.low[u.p] + ((int64_t(sq) * a.L + u.l) * rps + m % rps) * R;
+          h[j] = lora.low + ((int64_t(sq) * a.L + u.l) * rps + m % rps) * R;
           x[j] = 0.f;
         }
 #pragma unroll 1
@@ -529,7 +546,8 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
   }
 }
 
-// low[p][b][l][row][r] = scale (A x), a CTA per (sequence, layer), problem and 8 NT of the rank.
+// low = scale (A x), a CTA per (sequence, layer) and 8 NT of the rank, and one for its boundary row
+// (the whole rank, and its outputs).
 // Its bytes (x and A once each) are few beside the weights'; what counts is the latency, as the
 // projections' kernel follows: 16 warps spread over the hidden size, 32 entries at a time (a
 // thread's 16-byte load of eight entries of a row is its part of two m16n8k16 products' operands,
@@ -537,6 +555,7 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
 // added in warp order. (Run beside the projections instead, a warp per 8 of the rank and no shared
 // memory, it took longer than their first units: 160 us instead of 82 for 16 requests at rank 16.)
 constexpr int kLowWarps = 16;
+constexpr int kLoraMaxRank = 128;
 
 __device__ inline void mma_bf16_warp(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1) {
@@ -552,82 +571,106 @@ __device__ inline void mma_bf16_warp(float (&c)[4], uint32_t a0, uint32_t a1, ui
 template <int MT, int NT>
 __global__ void __launch_bounds__(kLowWarps * 32) lora_low_kernel(const __grid_constant__ PLora lora, const __nv_bfloat16* x,
                                                                   const __nv_bfloat16* boundary, int L, int B,
-                                                                  int hidden, int32_t* err) {
+                                                                  int hidden, int n_kv, int32_t* err) {
   __shared__ __align__(16) float red[kLowWarps][16][8 * NT + 2];
-  const int b = int(blockIdx.x) / L, l = int(blockIdx.x) - b * L, p = blockIdx.y, r0 = int(blockIdx.z) * 8 * NT;
+  __shared__ float low_s[kLoraMaxRank];
+  const int R = lora.bank.rank;
+  const int b = int(blockIdx.x) / L, l = int(blockIdx.x) - b * L;
+  const int p = blockIdx.y + 1 == gridDim.y;  // the last CTA of a (sequence, layer): its boundary row, the whole rank
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int R = lora.bank.rank, rows = p ? 1 : B, nr = min(8 * NT, R - r0);
+  const int rows = p ? 1 : B;
   grid_dependency_wait();
   allow_dependent_launch();
   const int ad = lora.bank.adapter_of[b];
-  float* low = lora.low[p] + (int64_t(b) * L + l) * rows * R + r0;
-  __nv_bfloat16* split = p == 0 && lora.split ? lora.split + (int64_t(b) * L + l) * 2 * B * R + r0 : nullptr;
   if (ad < 0 || ad >= lora.bank.n_adapters) {  // none: its place is read by the epilogue and left out
     if (ad != -1 && threadIdx.x == 0) set_err(err, LS_DEVERR_ADAPTER);
     return;
   }
   const __nv_bfloat16* src = (p ? boundary : x) + (int64_t(b) * L + l) * rows * hidden + t * 8;
-  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p ? lora.bank.a_kv : lora.bank.a_q) +
-                           ((int64_t(ad) * L + l) * R + r0) * hidden + t * 8;
-  float acc[MT][NT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-  const __nv_bfloat16 *xr[2 * MT], *wr[NT];
+  const __nv_bfloat16* bank = static_cast<const __nv_bfloat16*>(p ? lora.bank.a_kv : lora.bank.a_q) +
+                              (int64_t(ad) * L + l) * R * hidden + t * 8;
+  // (rows past the last are read as the last one again and not stored)
+  const __nv_bfloat16* xr[2 * MT];
 #pragma unroll
   for (int m = 0; m < 2 * MT; ++m) xr[m] = src + int64_t(min(m * 8 + g, rows - 1)) * hidden;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) wr[n] = w + int64_t(min(8 * n + g, nr - 1)) * hidden;
-  constexpr int kAhead = 2 * MT + NT <= 4 ? 4 : 2;  // steps whose loads are in flight together
-  for (int k0 = warp * 32; k0 < hidden; k0 += 32 * kLowWarps * kAhead) {
-    uint4 av[kAhead][2 * MT], bv[kAhead][NT];
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
-      const int k = min(k0 + 32 * kLowWarps * s, hidden - 32);
-#pragma unroll
-      for (int m = 0; m < 2 * MT; ++m) av[s][m] = ld_nc_v4(xr[m] + k);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) bv[s][n] = ld_nc_v4(wr[n] + k);
-    }
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
-      if (k0 + 32 * kLowWarps * s >= hidden) break;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma_bf16_warp(acc[m][n], av[s][2 * m].x, av[s][2 * m + 1].x, av[s][2 * m].y, av[s][2 * m + 1].y, bv[s][n].x, bv[s][n].y);
-          mma_bf16_warp(acc[m][n], av[s][2 * m].z, av[s][2 * m + 1].z, av[s][2 * m].w, av[s][2 * m + 1].w, bv[s][n].z, bv[s][n].w);
-        }
-    }
-  }
   const float scale = lora.bank.scale[ad];
+  __nv_bfloat16* split = lora.split + (int64_t(b) * L + l) * 2 * B * R;
+  float* low = lora.low + (int64_t(b) * L + l) * B * R;
+  for (int r0 = p ? 0 : int(blockIdx.y) * 8 * NT; r0 < R; r0 += 8 * NT) {
+    const int nr = min(8 * NT, R - r0);
+    const __nv_bfloat16* wr[NT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (m > 0) __syncthreads();
+    for (int n = 0; n < NT; ++n) wr[n] = bank + int64_t(r0 + min(8 * n + g, nr - 1)) * hidden;
+    float acc[MT][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      *reinterpret_cast<float2*>(&red[warp][g][8 * n + 2 * t]) = make_float2(acc[m][n][0], acc[m][n][1]);
-      *reinterpret_cast<float2*>(&red[warp][g + 8][8 * n + 2 * t]) = make_float2(acc[m][n][2], acc[m][n][3]);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * nr; i += kLowWarps * 32) {
-      const int row = i / nr, r = i - row * nr;
-      if (16 * m + row >= rows) break;
-      float sum = 0.f;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int v = 0; v < kLowWarps; ++v) sum += red[v][row][r];
-      sum *= scale;
-      if (split) {
-        const __nv_bfloat16 hi = __float2bfloat16_rn(sum);
-        const float rest = sum - __bfloat162float(hi);
-        split[(16 * m + row) * R + r] = hi;
-        split[(B + 16 * m + row) * R + r] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.f);  // (an infinite sum stays infinite)
-      } else {
-        low[(16 * m + row) * R + r] = sum;
+      for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+    constexpr int kAhead = 2 * MT + NT <= 4 ? 4 : 2;  // steps whose loads are in flight together
+    for (int k0 = warp * 32; k0 < hidden; k0 += 32 * kLowWarps * kAhead) {
+      uint4 av[kAhead][2 * MT], bv[kAhead][NT];
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const int k = min(k0 + 32 * kLowWarps * s, hidden - 32);
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) av[s][m] = ld_nc_v4(xr[m] + k);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) bv[s][n] = ld_nc_v4(wr[n] + k);
+      }
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        if (k0 + 32 * kLowWarps * s >= hidden) break;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            mma_bf16_warp(acc[m][n], av[s][2 * m].x, av[s][2 * m + 1].x, av[s][2 * m].y, av[s][2 * m + 1].y, bv[s][n].x, bv[s][n].y);
+            mma_bf16_warp(acc[m][n], av[s][2 * m].z, av[s][2 * m + 1].z, av[s][2 * m].w, av[s][2 * m + 1].w, bv[s][n].z, bv[s][n].w);
+          }
       }
     }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        *reinterpret_cast<float2*>(&red[warp][g][8 * n + 2 * t]) = make_float2(acc[m][n][0], acc[m][n][1]);
+        *reinterpret_cast<float2*>(&red[warp][g + 8][8 * n + 2 * t]) = make_float2(acc[m][n][2], acc[m][n][3]);
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 16 * nr; i += kLowWarps * 32) {
+        const int row = 16 * m + i / nr, r = i % nr;
+        if (row >= rows) break;
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < kLowWarps; ++v) sum += red[v][i / nr][r];
+        sum *= scale;
+        if (p) {
+          low_s[r0 + r] = sum;
+        } else if (lora.split) {
+          const __nv_bfloat16 hi = __float2bfloat16_rn(sum);
+          const float rest = sum - __bfloat162float(hi);
+          split[row * R + r0 + r] = hi;
+          split[(B + row) * R + r0 + r] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.f);  // (an infinite sum stays infinite)
+        } else {
+          low[row * R + r0 + r] = sum;
+        }
+      }
+      __syncthreads();
+    }
+    if (!p) return;
+  }
+  // the boundary row's outputs, a weight row per thread
+  const __nv_bfloat16* wb = static_cast<const __nv_bfloat16*>(lora.bank.b_kv) + (int64_t(ad) * L + l) * n_kv * R;
+  for (int n = threadIdx.x; n < n_kv; n += kLowWarps * 32) {
+    float y = 0.f;
+#pragma unroll 4
+    for (int e = 0; e < R; e += 8) {
+      float f[8];
+      Elem<__nv_bfloat16>::to_f32(ld_nc_v4(wb + int64_t(n) * R + e), f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) y = fmaf(f[q], low_s[e + q], y);
+    }
+    lora.add[(int64_t(b) * L + l) * n_kv + n] = y;
   }
 }
 
@@ -646,7 +689,9 @@ bool encode_bf16(void* base, int rank, const cuuint64_t* dims, const cuuint64_t*
 bool prologue_supported(const Dev& p) { return prologue_shapes_ok(p.dtype, p.hidden, p.Hq, p.Hkv, p.D, p.B); }
 
 size_t lora_workspace_bytes(const ls_config& c, int rank) {
-  return size_t(align256(int64_t(c.batch) * c.n_layers * (c.block + 1) * rank * 4));
+  // low (or split) of the block rows, then the boundary rows' finished sums
+  const int64_t bl = int64_t(c.batch) * c.n_layers;
+  return size_t(align256(bl * c.block * rank * 4) + align256(bl * 2 * c.n_kv_heads * c.head_dim * 4));
 }
 
 cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, const void* x, const ls_lora* lora,
@@ -715,8 +760,8 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
   CUtensorMap mwl = mw0, mxl = mx0;  // (unused without adapters)
   if (lora) {
     pl.bank = *lora;
-    pl.low[0] = static_cast<float*>(low);
-    pl.low[1] = pl.low[0] + int64_t(p.b) * p.L * p.B * lora->rank;
+    pl.low = static_cast<float*>(low);
+    pl.add = reinterpret_cast<float*>(static_cast<char*>(low) + align256(int64_t(p.b) * p.L * p.B * lora->rank * 4));
     if (p.B % 16 == 0) {
       // the tiles' inner extent is 64 of the rank; what lies past it reads as zeros
       pl.split = static_cast<__nv_bfloat16*>(low);  // (two bf16 parts in the place of fp32 sums)
@@ -731,7 +776,7 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
     }
     cudaLaunchConfig_t lc{};
     const int tiles = lora->rank <= 8 ? 1 : (lora->rank <= 16 ? 2 : 4);  // (x is read again for each 32 of the rank)
-    lc.gridDim = dim3(p.b * p.L, 2, (lora->rank + 8 * tiles - 1) / (8 * tiles));
+    lc.gridDim = dim3(p.b * p.L, (lora->rank + 8 * tiles - 1) / (8 * tiles) + 1);
     lc.blockDim = dim3(kLowWarps * 32);
     lc.stream = stream;
     cudaLaunchAttribute la[1];
@@ -745,7 +790,7 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
                                          : (two ? lora_low_kernel<2, 4> : lora_low_kernel<1, 4>);
     e = cudaLaunchKernelEx(&lc, low_kernel, pl,
                            static_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(p.boundary),
-                           p.L, p.B, p.hidden, p.err);
+                           p.L, p.B, p.hidden, K.n_out, p.err);
     if (e != cudaSuccess) return e;
   }
   int grid = sms < kProMaxGrid ? sms : kProMaxGrid;
