@@ -233,10 +233,23 @@ def _ptr(x):
     raise TypeError(f"expected a tensor or an address, got {type(x)}")
 
 
+def _current_stream():
+    """The address of torch's current stream on the current device. (A Stream object per call
+    takes longer than the call itself; the raw getter is bound on first use, so that the package
+    loads without torch.)"""
+    global _current_stream
+    import torch
+    device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    torch.cuda.current_stream()  # initialises torch's CUDA state
+
+    def _current_stream():
+        return raw(device())
+    return _current_stream()
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -554,7 +554,8 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
 // their k order is free), with the loads of several steps in flight at once. The warps' sums are
 // added in warp order. (Run beside the projections instead, a warp per 8 of the rank and no shared
 // memory, it took longer than their first units: 160 us instead of 82 for 16 requests at rank 16.)
-constexpr int kLowWarps = 16;
+// (two CTAs per SM with 8 warps where the loads in flight need the registers)
+__host__ __device__ constexpr int low_warps(int nt) { return nt <= 2 ? 16 : 8; }
 constexpr int kLoraMaxRank = 128;
 
 __device__ inline void mma_bf16_warp(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -569,9 +570,10 @@ __device__ inline void mma_bf16_warp(float (&c)[4], uint32_t a0, uint32_t a1, ui
 // and rank entries past the last are read as the last one again and not stored: with a branch
 // per tile the loads would wait for one another.)
 template <int MT, int NT>
-__global__ void __launch_bounds__(kLowWarps * 32) lora_low_kernel(const __grid_constant__ PLora lora, const __nv_bfloat16* x,
+__global__ void __launch_bounds__(low_warps(NT) * 32) lora_low_kernel(const __grid_constant__ PLora lora, const __nv_bfloat16* x,
                                                                   const __nv_bfloat16* boundary, int L, int B,
                                                                   int hidden, int n_kv, int32_t* err) {
+  constexpr int kLowWarps = low_warps(NT);
   __shared__ __align__(16) float red[kLowWarps][16][8 * NT + 2];
   __shared__ float low_s[kLoraMaxRank];
   const int R = lora.bank.rank;
@@ -777,7 +779,7 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
     cudaLaunchConfig_t lc{};
     const int tiles = lora->rank <= 8 ? 1 : (lora->rank <= 16 ? 2 : 4);  // (x is read again for each 32 of the rank)
     lc.gridDim = dim3(p.b * p.L, (lora->rank + 8 * tiles - 1) / (8 * tiles) + 1);
-    lc.blockDim = dim3(kLowWarps * 32);
+    lc.blockDim = dim3(low_warps(tiles) * 32);
     lc.stream = stream;
     cudaLaunchAttribute la[1];
     la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
