@@ -201,6 +201,67 @@ __device__ inline bool ver_wait_warp(S& s, uint64_t* bar, uint32_t parity, int32
   return __all_sync(0xffffffffu, ok);
 }
 
+// The producer warp of both tensor-core kernels: a CTA's chunks, in order, into a ring of kRing
+// stages. A stage holds blocks of min(page_size, 128) rows as a page does (K codes, V codes, K
+// scales, V scales): a page's block of a KV head is one bulk copy, of a 256-row page the chunk's
+// half is copied section by section. A lane looks its page up one chunk before it is copied (always
+// a load, of the first entry where there is none: a value chosen after a load waits for it at once).
+template <int D, int kRing, typename S>
+__device__ inline void ver_produce(const VerArgs& a, S& s, uint64_t* full, uint64_t* empty, unsigned char* ring) {
+  constexpr int kStage = kVerChunk * (D + D / 8);
+  const int lane = threadIdx.x & 31;
+  const int ps = min(a.page_size, kVerChunk), pshift = min(a.page_shift, 7);
+  const bool wide = a.page_size > kVerChunk;
+  const int lanes = wide ? 4 : kVerChunk >> pshift;
+  VerCursor cur = ver_begin(a, blockIdx.x);
+  VerPiece p;
+  const int total = int(cur.left);
+  int64_t pos = 0;  // of this lane's page in the chunk looked up
+  int left = 0, k = 0;
+  int32_t entry = 0;
+  auto look_up = [&]() {
+    if (left == 0) {
+      if (!ver_next(a, cur, p)) return;
+      left = int(p.c1 - p.c0);
+      pos = p.c0 * kVerChunk + (wide ? 0 : int64_t(lane) << pshift);
+    }
+    entry = __ldg(a.table + (lane < lanes && pos < p.len ? int64_t(p.b) * a.max_blocks + (pos >> a.page_shift) : 0));
+  };
+  look_up();
+  for (; k < total; ++k) {
+    const bool held = lane < lanes && pos < p.len;
+    int64_t page = entry;
+    if (page < 0 || page >= a.num_pages) {  // flagged, and read as page 0
+      if (held) set_err(a.err, LS_DEVERR_PAGE);
+      page = 0;
+    }
+    const unsigned char* block = a.base + page * a.page_stride + int64_t(p.hm) * kv4_block_bytes(a.page_size, D);
+    const int first = int(pos) & (a.page_size - 1);
+    --left;
+    pos += kVerChunk;
+    look_up();
+    const int st = k % kRing;
+    if (k >= kRing && !ver_wait_warp(s, &empty[st], uint32_t(k / kRing - 1) & 1, a.err)) break;
+    unsigned char* dst = ring + st * kStage;
+    const int n = __popc(__ballot_sync(0xffffffffu, held));
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], uint32_t(wide ? kStage : n * kv4_block_bytes(ps, D)));
+    __syncwarp();
+    if (wide) {
+      if (lane < 4) {  // 128 of the page's rows: codes (lanes 0, 1) and scales (2, 3)
+        const int row = lane < 2 ? D / 2 : D / kKv4Group, bytes = kVerChunk * row;
+        const int64_t from = (lane < 2 ? 0 : int64_t(a.page_size) * D) + int64_t((lane & 1) * a.page_size + first) * row;
+        bulk_g2s(dst + (lane < 2 ? 0 : kVerChunk * D) + (lane & 1) * bytes, block + from, bytes, &full[st]);
+      }
+    } else if (held) {
+      bulk_g2s(dst + lane * kv4_block_bytes(ps, D), block, kv4_block_bytes(ps, D), &full[st]);
+    }
+  }
+  // after an abort: the copies in flight land before the shared memory is released
+  if (lane == 0 && *reinterpret_cast<volatile uint32_t*>(&s.abort))
+    for (int x = k > kRing ? k - kRing : 0; x < k; ++x)
+      mbar_wait_bounded(&full[x % kRing], uint32_t(x / kRing) & 1, kWaitLimit);
+}
+
 // A launch that may start while the kernel before it on the stream still runs: the kernels here
 // wait for it (grid_dependency_wait) before they read or write anything.
 template <typename... A>

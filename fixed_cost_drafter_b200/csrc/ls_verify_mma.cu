@@ -88,58 +88,15 @@ __global__ void __launch_bounds__(kMThreads) verify_mma_kernel(const VerArgs a) 
   __syncthreads();
   grid_dependency_wait();
   allow_dependent_launch();
-  VerCursor cur = ver_begin(a, blockIdx.x);
-  VerPiece p;
-  int k = 0;  // chunks so far: stage and phase
-
   if (warp == kMWarps) {
-    // ---------------------------------------------------------------- producer
-    bool ok = true;
-    while (ok && ver_next(a, cur, p)) {
-      // this lane's page of a chunk (one lane per page; of a 256-row page, its four sections)
-      const int lanes = a.page_size > kVerChunk ? 4 : kVerChunk >> pshift;
-      auto block_of = [&](int64_t c) -> const unsigned char* {
-        const int64_t pos = c * kVerChunk + (a.page_size > kVerChunk ? 0 : int64_t(lane) << pshift);
-        return lane < lanes && pos < p.len ? ver_block(a, p.b, pos >> a.page_shift, p.hm) : nullptr;
-      };
-      const unsigned char* next = block_of(p.c0);
-      for (int64_t c = p.c0; c < p.c1; ++c, ++k) {
-        const unsigned char* block = next;
-        if (c + 1 < p.c1) next = block_of(c + 1);
-        const int st = k % kMStages;
-        if (k >= kMStages &&
-            !ver_wait_warp(s, &s.empty[st], uint32_t(k / kMStages - 1) & 1, a.err)) {
-          ok = false;
-          break;
-        }
-        unsigned char* dst = ring + st * stage_bytes(D);
-        const int n = __popc(__ballot_sync(0xffffffffu, block != nullptr));
-        if (a.page_size > kVerChunk) {
-          if (lane == 0) mbar_arrive_expect_tx(&s.full[st], stage_bytes(D));
-          __syncwarp();
-          if (lane < 4) {
-            // sections of 128 of the page's rows: codes (lanes 0, 1) and scales (2, 3)
-            const int row = lane < 2 ? D / 2 : D / kKv4Group, bytes = kVerChunk * row;
-            const int64_t from = (lane < 2 ? 0 : int64_t(a.page_size) * D) + int64_t(lane & 1) * a.page_size * row +
-                                 (c * kVerChunk & (a.page_size - 1)) * row;
-            bulk_g2s(dst + (lane < 2 ? 0 : kVerChunk * D) + (lane & 1) * bytes, block + from, bytes, &s.full[st]);
-          }
-        } else {
-          const int bytes = kv4_block_bytes(ps, D);
-          if (lane == 0) mbar_arrive_expect_tx(&s.full[st], uint32_t(n * bytes));
-          __syncwarp();
-          if (block) bulk_g2s(dst + lane * bytes, block, bytes, &s.full[st]);
-        }
-      }
-    }
-    // after an abort: the copies in flight land before the shared memory is released
-    if (lane == 0 && *reinterpret_cast<volatile uint32_t*>(&s.abort))
-      for (int i = k > kMStages ? k - kMStages : 0; i < k; ++i)
-        mbar_wait_bounded(&s.full[i % kMStages], uint32_t(i / kMStages) & 1, kWaitLimit);
+    ver_produce<D, kMStages>(a, s, s.full, s.empty, ring);
     return;
   }
 
   // ------------------------------------------------------------------ consumers
+  VerCursor cur = ver_begin(a, blockIdx.x);
+  VerPiece p;
+  int k = 0;  // chunks so far: stage and phase
   const int g = lane >> 2, t = lane & 3;
   bool ok = true;
   while (ver_next(a, cur, p)) {

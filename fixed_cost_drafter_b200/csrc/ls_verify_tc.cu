@@ -277,44 +277,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
     }
   } else if (warp == kTLoadWarp) {
     // ---------------------------------------------------------------- producer
-    const int ps = min(a.page_size, kVerChunk), pshift = min(a.page_shift, 7);
-    const bool wide = a.page_size > kVerChunk;  // a chunk is half of a 256-row page: its four sections
-    const int lanes = wide ? 4 : kVerChunk >> pshift;
-    VerCursor cur = ver_begin(a, blockIdx.x);
-    VerPiece p;
-    int k = 0;
-    bool ok = true;
-    while (ok && ver_next(a, cur, p)) {
-      auto block_of = [&](int64_t c) -> const unsigned char* {  // this lane's page of a chunk
-        const int64_t pos = c * kVerChunk + (wide ? 0 : int64_t(lane) << pshift);
-        return lane < lanes && pos < p.len ? ver_block(a, p.b, pos >> a.page_shift, p.hm) : nullptr;
-      };
-      const unsigned char* next = block_of(p.c0);
-      for (int64_t c = p.c0; c < p.c1; ++c, ++k) {
-        const unsigned char* block = next;
-        if (c + 1 < p.c1) next = block_of(c + 1);
-        const int rs = k % kTRing;
-        if (k >= kTRing && !ver_wait_warp(s, &s.raw_empty[rs], uint32_t(k / kTRing - 1) & 1, a.err)) { ok = false; break; }
-        unsigned char* dst = ring + rs * kRaw;
-        const int n = __popc(__ballot_sync(0xffffffffu, block != nullptr));
-        if (lane == 0) mbar_arrive_expect_tx(&s.raw_full[rs], uint32_t(wide ? kRaw : n * kv4_block_bytes(ps, D)));
-        __syncwarp();
-        if (wide) {
-          if (lane < 4) {  // 128 of the page's rows: codes (lanes 0, 1) and scales (2, 3)
-            const int row = lane < 2 ? D / 2 : D / kKv4Group, bytes = kVerChunk * row;
-            const int64_t from = (lane < 2 ? 0 : int64_t(a.page_size) * D) + int64_t(lane & 1) * a.page_size * row +
-                                 (c * kVerChunk & (a.page_size - 1)) * row;
-            bulk_g2s(dst + (lane < 2 ? 0 : kVerChunk * D) + (lane & 1) * bytes, block + from, bytes, &s.raw_full[rs]);
-          }
-        } else if (block) {
-          bulk_g2s(dst + lane * kv4_block_bytes(ps, D), block, kv4_block_bytes(ps, D), &s.raw_full[rs]);
-        }
-      }
-    }
-    // after an abort: the copies in flight land before the shared memory is released
-    if (lane == 0 && *reinterpret_cast<volatile uint32_t*>(&s.abort))
-      for (int x = k > kTRing ? k - kTRing : 0; x < k; ++x)
-        mbar_wait_bounded(&s.raw_full[x % kTRing], uint32_t(x / kTRing) & 1, kWaitLimit);
+    ver_produce<D, kTRing>(a, s, s.raw_full, s.raw_empty, ring);
   } else if (warp == kTQkWarp || warp == kTPvWarp) {
     // ---------------------------------------------------------------- MMA issuers
     // the whole warp walks the chunks; one elected lane issues
