@@ -18,6 +18,7 @@ namespace ls {
 namespace {
 
 constexpr int kPagesThreads = 256;
+constexpr int kPagesAhead = 4;  // rows per thread whose page ids are loaded together
 
 struct PagesArgs {
   ls_page_pool pool;
@@ -176,16 +177,53 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
   const int64_t room = packed ? a.capacity - first_row : a.max_rows;
   const int n_out = packed ? me.n : a.max_rows;
   if (packed && n_out > room) bits |= LS_DEVERR_POOL;
-  for (int r = x * kPagesThreads + tid; r < n_out && r < room; r += a.chunks * kPagesThreads) {
-    int64_t slot = -1;
-    if (served && r < me.n) {
-      int off;
-      const int64_t pi = split_pos(me.len + r, ps, off);
-      const int64_t page = pi < me.held ? table[pi] : top[-(pi - me.held)];
-      if (page < 0 || page >= a.pool.num_pages) bits |= LS_DEVERR_PAGE;
-      else slot = page * ps + off;
+  // four rows' pages are loaded together: each slot waits for its page's id
+  const int step = a.chunks * kPagesThreads, n_write = int(n_out < room ? n_out : (room > 0 ? room : 0));
+  const int64_t end = me.len + me.n;
+  const bool simple = (ps & (ps - 1)) == 0 && end < (int64_t(1) << 31);  // 32-bit positions, shifts
+  const int shift = __ffs(ps) - 1, len32 = int(me.len);
+  if (simple) {
+    for (int r0 = x * kPagesThreads + tid; r0 < n_write; r0 += kPagesAhead * step) {
+      int32_t page[kPagesAhead];
+#pragma unroll
+      for (int u = 0; u < kPagesAhead; ++u) {
+        const int r = r0 + u * step, pi = (len32 + r) >> shift;
+        page[u] = served && r < me.n ? (pi < me.held ? table[pi] : top[me.held - pi]) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kPagesAhead; ++u) {
+        const int r = r0 + u * step;
+        if (r >= n_write) break;
+        const bool ok = page[u] >= 0 && page[u] < a.pool.num_pages;
+        if (!ok && served && r < me.n) bits |= LS_DEVERR_PAGE;
+        slots[r] = ok ? (int64_t(page[u]) << shift) + ((len32 + r) & (ps - 1)) : -1;
+      }
     }
-    slots[r] = slot;
+  }
+  for (int r0 = simple ? n_write : x * kPagesThreads + tid; r0 < n_write; r0 += kPagesAhead * step) {
+    int64_t page[kPagesAhead];
+    int off[kPagesAhead];
+#pragma unroll
+    for (int u = 0; u < kPagesAhead; ++u) {
+      const int r = r0 + u * step;
+      page[u] = -1;
+      off[u] = -1;
+      if (served && r < me.n && r < n_write) {
+        const int64_t pi = split_pos(me.len + r, ps, off[u]);
+        page[u] = pi < me.held ? table[pi] : top[-(pi - me.held)];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kPagesAhead; ++u) {
+      const int r = r0 + u * step;
+      if (r >= n_write) break;
+      int64_t slot = -1;
+      if (off[u] >= 0) {
+        if (page[u] < 0 || page[u] >= a.pool.num_pages) bits |= LS_DEVERR_PAGE;
+        else slot = page[u] * ps + off[u];
+      }
+      slots[r] = slot;
+    }
   }
   if (packed && x == 0 && tid == 0) {
     a.row_begin[seq] = first_row;
@@ -238,11 +276,19 @@ __global__ void __launch_bounds__(kPagesThreads) pages_trim_kernel(const PagesAr
   if (ok) {
     int32_t* table = a.pool.block_table + int64_t(seq) * a.pool.max_blocks + (me.held - me.pages);
     int32_t* top = a.pool.free_pages + (count + total - 1 - before);
-    for (int j = x * kPagesThreads + tid; j < me.pages; j += a.chunks * kPagesThreads) {
-      const int32_t id = table[j];
-      if (id < 0 || id >= a.pool.num_pages) bits |= LS_DEVERR_PAGE;
-      top[-j] = id;
-      table[j] = -1;
+    const int step = a.chunks * kPagesThreads;
+    for (int j0 = x * kPagesThreads + tid; j0 < me.pages; j0 += kPagesAhead * step) {
+      int32_t id[kPagesAhead];
+#pragma unroll
+      for (int u = 0; u < kPagesAhead; ++u) id[u] = table[min(j0 + u * step, me.pages - 1)];
+#pragma unroll
+      for (int u = 0; u < kPagesAhead; ++u) {
+        const int j = j0 + u * step;
+        if (j >= me.pages) break;
+        if (id[u] < 0 || id[u] >= a.pool.num_pages) bits |= LS_DEVERR_PAGE;
+        top[-j] = id[u];
+        table[j] = -1;
+      }
     }
   }
   if (bits) set_err(a.err, bits);
@@ -265,11 +311,11 @@ PagesArgs pages_args(const Dev& p, const ls_page_pool& pool, const int64_t* len)
   return a;
 }
 
-// CTAs per sequence for `items` entries of work each: eight items a thread, at most about
-// eight CTAs an SM in all.
+// CTAs per sequence for `items` entries of work each: four items a thread, at most about
+// sixteen CTAs an SM in all (sequences' lengths differ: the longest counts).
 int chunks_for(int64_t items, int b, int sms) {
-  const int64_t want = (items + 8 * kPagesThreads - 1) / (8 * kPagesThreads);
-  const int64_t most = max(1, 8 * sms / b);
+  const int64_t want = (items + 4 * kPagesThreads - 1) / (4 * kPagesThreads);
+  const int64_t most = max(1, 16 * sms / b);
   return int(want < 1 ? 1 : (want < most ? want : most));
 }
 
