@@ -285,4 +285,21 @@ __device__ inline const char* paged_slot(const ls_paged_kv& kv, const char* base
   return base + (page * kv.page_stride + int64_t(off) * kv.slot_stride) * elem;
 }
 
+// A launch that may start while the kernel before it on the stream still runs: the kernel waits for
+// it (grid_dependency_wait) before it reads or writes anything, then lets its own successor start.
+template <typename... A>
+inline cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace ls

@@ -94,6 +94,8 @@ __device__ inline bool kv4_place(const Kv4Args& a, int vec, int64_t& row, int& e
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Args a) {
   using E = Elem<T>;
+  grid_dependency_wait();
+  allow_dependent_launch();
   constexpr int kVec = E::kVec, kLanes = kKv4Group / kVec;  // threads per scale group
   int64_t row;
   int e;
@@ -138,6 +140,8 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Args a
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Args a) {
   using E = Elem<T>;
+  grid_dependency_wait();
+  allow_dependent_launch();
   constexpr int kVec = E::kVec;
   int64_t row;
   int e;
@@ -201,9 +205,8 @@ cudaError_t launch_kv4_append(const Dev& p, const ls_paged_kv4& kv, int layer, c
   const int64_t blocks = (n_rows + a.per_cta - 1) / a.per_cta;
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
   const unsigned grid = static_cast<unsigned>(blocks);
-  if (p.dtype == LS_BF16) kv4_append_kernel<__nv_bfloat16><<<grid, threads, 0, stream>>>(a);
-  else kv4_append_kernel<float><<<grid, threads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return p.dtype == LS_BF16 ? launch_overlapped(kv4_append_kernel<__nv_bfloat16>, dim3(grid), threads, 0, stream, a)
+                            : launch_overlapped(kv4_append_kernel<float>, dim3(grid), threads, 0, stream, a);
 }
 
 cudaError_t launch_kv4_read(const Dev& p, const ls_paged_kv4& kv, int layer, const int64_t* slots, int64_t n_rows,
@@ -213,9 +216,8 @@ cudaError_t launch_kv4_read(const Dev& p, const ls_paged_kv4& kv, int layer, con
   const int64_t blocks = (n_rows + a.per_cta - 1) / a.per_cta;
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
   const unsigned grid = static_cast<unsigned>(blocks);
-  if (p.dtype == LS_BF16) kv4_read_kernel<__nv_bfloat16><<<grid, threads, 0, stream>>>(a);
-  else kv4_read_kernel<float><<<grid, threads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return p.dtype == LS_BF16 ? launch_overlapped(kv4_read_kernel<__nv_bfloat16>, dim3(grid), threads, 0, stream, a)
+                            : launch_overlapped(kv4_read_kernel<float>, dim3(grid), threads, 0, stream, a);
 }
 
 }  // namespace ls

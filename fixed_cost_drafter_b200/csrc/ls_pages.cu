@@ -18,7 +18,7 @@ namespace ls {
 namespace {
 
 constexpr int kPagesThreads = 256;
-constexpr int kPagesAhead = 4;  // rows per thread whose page ids are loaded together
+constexpr int kPagesAhead = 8;  // rows per thread whose page ids are loaded together
 
 struct PagesArgs {
   ls_page_pool pool;
@@ -147,6 +147,8 @@ __device__ inline bool last_to_arrive(const PagesArgs& a) {
 }
 
 __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const PagesArgs a) {
+  grid_dependency_wait();
+  allow_dependent_launch();
   const int seq = int(blockIdx.x) / a.chunks, x = int(blockIdx.x) - seq * a.chunks;
   const int tid = threadIdx.x, ps = a.pool.page_size;
   const bool packed = a.row_begin != nullptr;
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
   const int64_t room = packed ? a.capacity - first_row : a.max_rows;
   const int n_out = packed ? me.n : a.max_rows;
   if (packed && n_out > room) bits |= LS_DEVERR_POOL;
-  // four rows' pages are loaded together: each slot waits for its page's id
+  // several rows' pages are loaded together: each slot waits for its page's id
   const int step = a.chunks * kPagesThreads, n_write = int(n_out < room ? n_out : (room > 0 ? room : 0));
   const int64_t end = me.len + me.n;
   const bool simple = (ps & (ps - 1)) == 0 && end < (int64_t(1) << 31);  // 32-bit positions, shifts
@@ -258,6 +260,8 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
 }
 
 __global__ void __launch_bounds__(kPagesThreads) pages_trim_kernel(const PagesArgs a) {
+  grid_dependency_wait();
+  allow_dependent_launch();
   const int seq = int(blockIdx.x) / a.chunks, x = int(blockIdx.x) - seq * a.chunks;
   const int tid = threadIdx.x;
   const SeqPlan me = plan_trim(a, seq);
@@ -311,11 +315,11 @@ PagesArgs pages_args(const Dev& p, const ls_page_pool& pool, const int64_t* len)
   return a;
 }
 
-// CTAs per sequence for `items` entries of work each: four items a thread, at most about
-// sixteen CTAs an SM in all (sequences' lengths differ: the longest counts).
+// CTAs per sequence for `items` entries of work each: eight items a thread, at most about four
+// CTAs an SM in all (more would spend their time on finding their place).
 int chunks_for(int64_t items, int b, int sms) {
-  const int64_t want = (items + 4 * kPagesThreads - 1) / (4 * kPagesThreads);
-  const int64_t most = max(1, 16 * sms / b);
+  const int64_t want = (items + 8 * kPagesThreads - 1) / (8 * kPagesThreads);
+  const int64_t most = max(1, 4 * sms / b);
   return int(want < 1 ? 1 : (want < most ? want : most));
 }
 
@@ -331,16 +335,14 @@ cudaError_t launch_pages_extend(const Dev& p, const ls_page_pool& pool, const in
   a.slots = slots;
   a.capacity = capacity;
   a.chunks = chunks_for(max_rows, p.b, sms);
-  pages_extend_kernel<<<p.b * a.chunks, kPagesThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(pages_extend_kernel, dim3(p.b * a.chunks), kPagesThreads, 0, stream, a);
 }
 
 cudaError_t launch_pages_trim(const Dev& p, const ls_page_pool& pool, const int64_t* len, int sms,
                               cudaStream_t stream) {
   PagesArgs a = pages_args(p, pool, len);
   a.chunks = chunks_for(pool.max_blocks, p.b, sms);
-  pages_trim_kernel<<<p.b * a.chunks, kPagesThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(pages_trim_kernel, dim3(p.b * a.chunks), kPagesThreads, 0, stream, a);
 }
 
 }  // namespace ls

@@ -318,16 +318,16 @@ cudaError_t launch_verify(const Dev& p, const ls_config& c, const ls_paged_kv4& 
   } else if (v.kernel == kVerTc) {
     e = launch_verify_tc(a, stream);
   } else if (p.dtype == LS_F32) {
-    e = p.D == 128 ? ver_launch(verify_simt_kernel<float, 128>, a.G, kVThreads, 0, stream, a)
-                   : ver_launch(verify_simt_kernel<float, 64>, a.G, kVThreads, 0, stream, a);
+    e = p.D == 128 ? launch_overlapped(verify_simt_kernel<float, 128>, a.G, kVThreads, 0, stream, a)
+                   : launch_overlapped(verify_simt_kernel<float, 64>, a.G, kVThreads, 0, stream, a);
   } else {
-    e = p.D == 128 ? ver_launch(verify_simt_kernel<__nv_bfloat16, 128>, a.G, kVThreads, 0, stream, a)
-                   : ver_launch(verify_simt_kernel<__nv_bfloat16, 64>, a.G, kVThreads, 0, stream, a);
+    e = p.D == 128 ? launch_overlapped(verify_simt_kernel<__nv_bfloat16, 128>, a.G, kVThreads, 0, stream, a)
+                   : launch_overlapped(verify_simt_kernel<__nv_bfloat16, 64>, a.G, kVThreads, 0, stream, a);
   }
   if (e != cudaSuccess) return e;
   const dim3 grid(p.b * a.HM, ((a.M < v.MR ? a.M : v.MR) + kVThreads / 32 - 1) / (kVThreads / 32));
-  return p.D == 128 ? ver_launch(verify_join_kernel<128>, grid, kVThreads, 0, stream, a)
-                    : ver_launch(verify_join_kernel<64>, grid, kVThreads, 0, stream, a);
+  return p.D == 128 ? launch_overlapped(verify_join_kernel<128>, grid, kVThreads, 0, stream, a)
+                    : launch_overlapped(verify_join_kernel<64>, grid, kVThreads, 0, stream, a);
 }
 
 }  // namespace ls

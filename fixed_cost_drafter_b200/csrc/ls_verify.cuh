@@ -262,21 +262,4 @@ __device__ inline void ver_produce(const VerArgs& a, S& s, uint64_t* full, uint6
       mbar_wait_bounded(&full[x % kRing], uint32_t(x / kRing) & 1, kWaitLimit);
 }
 
-// A launch that may start while the kernel before it on the stream still runs: the kernels here
-// wait for it (grid_dependency_wait) before they read or write anything.
-template <typename... A>
-inline cudaError_t ver_launch(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace ls

@@ -374,7 +374,7 @@ cudaError_t launch_mma(const VerArgs& a, cudaStream_t stream) {
   const int smem = kMStages * stage_bytes(D);
   const cudaError_t e = cudaFuncSetAttribute(verify_mma_kernel<NT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return ver_launch(verify_mma_kernel<NT, D>, a.G, kMThreads, smem, stream, a);
+  return launch_overlapped(verify_mma_kernel<NT, D>, a.G, kMThreads, smem, stream, a);
 }
 
 }  // namespace

@@ -550,7 +550,7 @@ cudaError_t launch_tc(const VerArgs& a, cudaStream_t stream) {
   constexpr int smem = 4 * kVerChunk * D * 2 + kTRing * kVerChunk * (D + D / 8) + 1024;
   const cudaError_t e = cudaFuncSetAttribute(verify_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return ver_launch(verify_tc_kernel<D>, a.G, kTThreads, smem, stream, a);
+  return launch_overlapped(verify_tc_kernel<D>, a.G, kTThreads, smem, stream, a);
 }
 
 }  // namespace
