@@ -235,16 +235,28 @@ __global__ void __launch_bounds__(kVThreads) verify_join_kernel(const VerArgs a)
       w = exp2f(ml.x - mu);
       sum = fmaf(w, ml.y, sum);
     }
+    // kBatch pieces' outputs are loaded together (past the last: that one again, with weight 0)
+    constexpr int kBatch = 8;
     const int cn = min(32, c_last - c0 + 1);
-#pragma unroll 8
-    for (int u = 0; u < cn; ++u) {
-      const float wu = __shfl_sync(0xffffffffu, w, u);
-      const float* src = a.part_o + at(c0 + u) * D + lane * kPer;
+    for (int u0 = 0; u0 < cn; u0 += kBatch) {
+      float x[kBatch][kPer];
 #pragma unroll
-      for (int e = 0; e < kPer; e += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(src + e);
-        o[e] = fmaf(wu, x.x, o[e]);
-        o[e + 1] = fmaf(wu, x.y, o[e + 1]);
+      for (int u = 0; u < kBatch; ++u) {
+        const float* src = a.part_o + at(c0 + min(u0 + u, cn - 1)) * D + lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(src + e));
+          x[u][e] = y.x;
+          x[u][e + 1] = y.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float wu = __shfl_sync(0xffffffffu, w, (u0 + u) & 31);
+        if (u0 + u < cn) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) o[e] = fmaf(wu, x[u][e], o[e]);
+        }
       }
     }
   }
