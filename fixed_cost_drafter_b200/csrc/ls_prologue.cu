@@ -220,7 +220,10 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-  if (warp != 0) {  // the weight producer waits once its first ring of weights is on its way
+  // With adapters the kernel before is lora_low_kernel, which lets this one start once everything
+  // before it has completed: only what it writes itself is waited for, by the epilogue (at its
+  // start) and by the producers before their first adapter step.
+  if (kLora ? warp >= 2 && warp <= 5 : warp != 0) {  // (the weight producer: once its first ring of weights is on its way)
     grid_dependency_wait();
     allow_dependent_launch();
   }
@@ -245,7 +248,7 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
   if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ TMA producers
     // warp 0: the weights (A) of every k-step; warp 6: the activations (B)
-    bool waited = warp != 0;
+    bool waited = !kLora && warp != 0;
     if (lane == 0) {
       const bool is_a = warp == 0;
       const int nst = is_a ? kPAStages : kPBStages;
@@ -264,7 +267,7 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
         // every weight tile of the layer) out of L2
         // k-step k's stage of this ring is free for its next copy (false: gave up)
         auto begin_step = [&](uint32_t n_bytes) -> bool {
-          if (k == nst && !waited) {  // (the first ring's weights are in flight)
+          if (!kLora && k == nst && !waited) {  // (the first ring's weights are in flight)
             grid_dependency_wait();
             allow_dependent_launch();
             waited = true;
@@ -289,14 +292,14 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
             tma_load_3d_hint(b_ring + st * kPBBytes, m, ks * kPKStep, u.l, u.mt * P.seq_per_unit, full, pol);
         }
         if (!ok) break;
-        if (kLora && !waited) {  // the adapters' ids and inner products are the kernel before's
-          grid_dependency_wait();
-          allow_dependent_launch();
-          waited = true;
-        }
         ok = adapter_steps(it, u, [&](int i, int ad, int rc) -> bool {
           const int st = k % nst;
           uint64_t* full = &s.afull[k % kPAStages];
+          if (!waited) {
+            grid_dependency_wait();
+            allow_dependent_launch();
+            waited = true;
+          }
           if (!begin_step(is_a ? uint32_t(kPABytes) : uint32_t(2 * P.rows_per_seq * kPKStep * 2))) return false;
           if (is_a)
             tma_load_2d(a_ring + st * kPABytes, &wl, rc, (ad * a.L + u.l) * P.n_out + u.nt * kPTileN, full);
@@ -360,6 +363,11 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
           });
         if (ok) mma_commit(&s.acc_full[ab]);
       }
+    }
+    if (kLora) {  // (every thread passes the wait before it triggers)
+      __syncwarp();
+      grid_dependency_wait();
+      allow_dependent_launch();
     }
   } else {
     // ------------------------------------------------------------ epilogue (warps 2-5)
