@@ -38,13 +38,13 @@ namespace ls {
 
 namespace {
 
-constexpr int kTThreads = 512;
+constexpr int kTThreads = 640;
 constexpr int kTQkWarp = 8, kTPvWarp = 9, kTLoadWarp = 10, kTConvWarp = 11;
-constexpr int kTRing = 4;          // stages of raw chunks
+constexpr int kTRing = 3;          // stages of raw chunks
 constexpr int kTUnit = 32;         // rows of a conversion task
 constexpr int kTUnits = kVerChunk / kTUnit;  // of a chunk's keys, and as many of its values
 constexpr int kTSub = 64;          // keys the softmax takes at a time
-constexpr uint32_t kTCols = 512, kTO = 256, kTQ = 384;
+constexpr uint32_t kTCols = 512, kTO = 256, kTP = 384;
 constexpr float kTRoom = 8.f;
 constexpr float kTMostSum = 32768.f;
 constexpr int kNanSlots = 4;       // pieces whose NaN positions are kept (conversion runs at most 2 ahead)
@@ -52,12 +52,12 @@ constexpr int kNanSlots = 4;       // pieces whose NaN positions are kept (conve
 struct TBars {
   uint64_t raw_full[kTRing], raw_empty[kTRing];
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-  uint64_t s_full[2], p_full[4], p_free[2];  // p_full: [buffer][half]
+  uint64_t s_full[2], s_free[2], p_full[4], p_free[2];  // p_full: [buffer][half]
   uint64_t h_done;  // the first half's P V
-  uint64_t decided[4][2];  // per softmax warp pair: the reference after an even / odd chunk
   uint64_t joined[4];      // both warps' sums of a piece
   uint64_t q_full, o_full, o_free, drain[2];
   uint32_t tmem_base, abort;
+  uint32_t turn[4];  // chunks whose reference is decided, per 32 rows
   int nan_at[kNanSlots][8];
   float ref[kTcRows];
   float2 state[2][2][kTcRows];  // [piece parity][warp group]: sum and reference of a row
@@ -74,8 +74,31 @@ __device__ inline bool elect_one() {
   return r != 0;
 }
 
-__device__ inline void tmem_st32u(uint32_t taddr, const uint32_t* v) {
-  tmem_st32(taddr, reinterpret_cast<const float*>(v));
+__device__ inline void tmem_st16u(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ inline void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The counter of decided chunks: passed on by a release store, polled with a bound.
+__device__ inline void turn_set(uint32_t* p, uint32_t v) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+}
+__device__ inline bool turn_wait(TBars& s, uint32_t* p, uint32_t v, int32_t* err) {
+  uint32_t x = 0;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(x) : "r"(smem_u32(p)) : "memory");
+    if (x == v || ((i & 1023) == 1023 && *reinterpret_cast<volatile uint32_t*>(&s.abort))) break;
+  }
+  if (x != v) {
+    if (!*reinterpret_cast<volatile uint32_t*>(&s.abort)) set_err(err, LS_DEVERR_WAIT_TIMEOUT);
+    *reinterpret_cast<volatile uint32_t*>(&s.abort) = 1;
+  }
+  return __all_sync(0xffffffffu, x == v);
 }
 
 __device__ inline float ex2a(float x) {
@@ -120,7 +143,8 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
   __shared__ TBars s;
   unsigned char* kbuf = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* vbuf = kbuf + 2 * kTile;
-  unsigned char* ring = vbuf + 2 * kTile;
+  unsigned char* qbuf = vbuf + 2 * kTile;       // [D / 64 halves][128 rows][128 B], as a K tile
+  unsigned char* ring = qbuf + kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int act = (a.M + 31) / 32;             // softmax warps with rows
   if (threadIdx.x == 0) {
@@ -137,6 +161,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.s_free[i], act);
       mbar_init(&s.p_full[2 * i], act);
       mbar_init(&s.p_full[2 * i + 1], act);
       mbar_init(&s.p_free[i], 1);
@@ -146,8 +171,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
     mbar_init(&s.h_done, 1);
     mbar_init(&s.o_free, 2 * act);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&s.decided[i][0], 1);
-      mbar_init(&s.decided[i][1], 1);
+      s.turn[i] = 0;
       mbar_init(&s.joined[i], 2);
     }
     s.abort = 0;
@@ -284,6 +308,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
     const bool qk = warp == kTQkWarp;
     VerCursor cur = ver_begin(a, blockIdx.x);
     VerPiece p;
+    const uint64_t descq = sdesc(smem_u32(qbuf), 16, 1024);
     const uint64_t desc0 = qk ? sdesc(smem_u32(kbuf), 16, 1024) : sdesc(smem_u32(vbuf), kHalf, 1024);
     bool ok = true;
     int k = 0;
@@ -304,13 +329,14 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
         const uint64_t desc = desc0 + uint32_t(st * kTile >> 4);
         if (!ver_wait_warp(s, qk ? &s.kfull[st] : &s.vfull[st], phase, a.err)) { ok = false; break; }
         if (qk) {
-          if (k >= 2 && !ver_wait_warp(s, &s.p_free[st], phase ^ 1, a.err)) { ok = false; break; }
+          if (k >= 2 && !ver_wait_warp(s, &s.s_free[st], phase ^ 1, a.err)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ta(sp, tmem + kTQ + 8 * kk, desc + uint32_t(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
-                          idesc_f16(kVerChunk, false), kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t step = uint32_t(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+              mma_bf16(sp, descq + step, desc + step, idesc_f16(kVerChunk, false), kk > 0);
+            }
             mma_commit(&s.s_full[st]);
             mma_commit(&s.kempty[st]);
           }
@@ -323,7 +349,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kTSub / 16; ++kk)
-                mma_bf16_ta(tmem + kTO, sp + 32 * h + 8 * kk, desc + uint32_t((h * kTSub + kk * 16) * 128 >> 4),
+                mma_bf16_ta(tmem + kTO, tmem + kTP + 64 * st + 32 * h + 8 * kk, desc + uint32_t((h * kTSub + kk * 16) * 128 >> 4),
                             idesc_f16(D, true), h == 1 || kk > 0 || c > 0);
               if (h == 0) {
                 mma_commit(&s.h_done);
@@ -368,21 +394,17 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
       const float f = ldexpf(a.scale_log2, ex);
       if (grp == 0) {
         const float down = ex == 127 ? 0x1p-127f : __uint_as_float(uint32_t(127 - ex) << 23);
-#pragma unroll 1
-        for (int h = 0; h < D / 64; ++h) {
-          uint32_t w[32];
+#pragma unroll 2
+        for (int c8 = 0; c8 < D / 8; ++c8) {
+          float x[8];
 #pragma unroll
-          for (int c8 = 0; c8 < 8; ++c8) {
-            float x[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) x[u] = 0.f;
-            if (real) Elem<__nv_bfloat16>::to_f32(ld_nc_v4(src + dim_of<D>(64 * h + 8 * c8)), x);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) w[4 * c8 + u] = pack_half2(x[2 * u] * down, x[2 * u + 1] * down);
-          }
-          tmem_st32u(trow + kTQ + 32 * h, w);
+          for (int u = 0; u < 8; ++u) x[u] = 0.f;
+          if (real) Elem<__nv_bfloat16>::to_f32(ld_nc_v4(src + dim_of<D>(8 * c8)), x);
+          *reinterpret_cast<uint4*>(qbuf + (c8 >> 3) * kHalf + m * 128 + (((c8 & 7) ^ (m & 7)) << 4)) =
+              make_uint4(pack_half2(x[0] * down, x[1] * down), pack_half2(x[2] * down, x[3] * down),
+                         pack_half2(x[4] * down, x[5] * down), pack_half2(x[6] * down, x[7] * down));
         }
-        tc_fence_before();
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.q_full);
       }
@@ -395,20 +417,23 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
       for (int c = 0; c < n && ok; ++c, ++k) {
         if ((k & 1) != grp) continue;
         const uint32_t phase = uint32_t(k >> 1) & 1;
-        if (!ver_wait_warp(s, &s.s_full[grp], phase, a.err)) { ok = false; break; }
+        // the P columns' last use, and the scores
+        ok = (k < 2 || ver_wait_warp(s, &s.p_free[grp], phase ^ 1, a.err)) && ver_wait_warp(s, &s.s_full[grp], phase, a.err);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const uint32_t sp = trow + kVerChunk * grp + kTSub * h;
           const int seen = limit - (c * kVerChunk + h * kTSub);
           const bool edge = __any_sync(0xffffffffu, seen < kTSub);
-          uint32_t w[32];
+          const uint32_t pp = trow + kTP + 64 * grp + 32 * h;
           float part;
-          auto weigh = [&]() {  // w: the 64 weights against ref; part: their sum
+          auto weigh = [&]() {  // P: the 64 weights against ref; part: their sum
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               float x[32];
+              uint32_t w[16];
               tmem_ld32(sp + 32 * b, x);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], f, -ref);
@@ -421,15 +446,16 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
                 x[e] = ex2a(x[e]);
                 x[e + 1] = ex2a(x[e + 1]);
                 add2(acc[e & 2], acc[(e & 2) + 1], x[e], x[e + 1]);
-                w[16 * b + e / 2] = pack_half2(x[e], x[e + 1]);
+                w[e / 2] = pack_half2(x[e], x[e + 1]);
               }
+              tmem_st16u(pp + 16 * b, w);
             }
             part = (acc[0] + acc[1]) + (acc[2] + acc[3]);
           };
           weigh();
           float now = ref;  // the row's reference so far
           if (h == 0 && c > 0) {
-            if (!ver_wait_warp(s, &s.decided[wp][grp ^ 1], uint32_t((k - 1) >> 1) & 1, a.err)) { ok = false; break; }
+            if (!turn_wait(s, &s.turn[wp], uint32_t(k), a.err)) { ok = false; break; }
             now = s.ref[m];
           }
           const bool move = !(part <= kTMostSum) || now != ref;
@@ -465,13 +491,16 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
             weigh();
           }
           sum += part;
-          tmem_st32u(trow + kVerChunk * grp + 32 * h, w);
           if (h == 1) s.ref[m] = ref;
+          tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&s.p_full[2 * grp + h]);
-            if (h == 1) mbar_arrive(&s.decided[wp][grp]);
+            if (h == 1) {
+              turn_set(&s.turn[wp], uint32_t(k) + 1);
+              mbar_arrive(&s.s_free[grp]);
+            }
           }
         }
       }
@@ -547,7 +576,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
 
 template <int D>
 cudaError_t launch_tc(const VerArgs& a, cudaStream_t stream) {
-  constexpr int smem = 4 * kVerChunk * D * 2 + kTRing * kVerChunk * (D + D / 8) + 1024;
+  constexpr int smem = 5 * kVerChunk * D * 2 + kTRing * kVerChunk * (D + D / 8) + 1024;
   const cudaError_t e = cudaFuncSetAttribute(verify_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_overlapped(verify_tc_kernel<D>, a.G, kTThreads, smem, stream, a);
