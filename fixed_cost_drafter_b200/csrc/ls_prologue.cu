@@ -54,8 +54,9 @@ constexpr uint32_t kPTmemCols = 512;
 struct PProblem {
   int32_t n_out;         // weight rows (output columns) per layer, a multiple of 128
   int32_t rows_per_seq;  // activation rows per sequence and layer: 1 (boundary) or B (block)
+  int32_t pitch;         // tile rows per sequence: rows_per_seq, with adapters rounded up to 16 (see PLora)
   int32_t seq_per_unit;  // sequences per activation tile
-  int32_t load_rows;     // activation rows of a tile's box: seq_per_unit * rows_per_seq
+  int32_t load_rows;     // activation rows of a tile's box: seq_per_unit * pitch
   int32_t act_rows;      // the MMA's N: load_rows rounded up to 16 (the rows past load_rows
                          // are stale shared memory feeding accumulator columns never stored)
   int32_t m_tiles;       // activation tiles: ceil(b / seq_per_unit)
@@ -76,16 +77,16 @@ struct PArgs {
 };
 
 // Low-rank adapters (ls_draft_prologue_lora): scale * (A x) of problem p, by lora_low_kernel.
-// Block queries whose blocks are whole 16-row steps of the MMA's N take them as further k-steps
-// of their unit: weight rows B_a of the sequence's adapter against split[], low as two bf16
-// parts (high + low: 16 bits of the fp32 sum), into the sequence's accumulator columns only. The
-// others are added by the epilogue in fp32, so that no adapter's infinities reach another
-// sequence: odd blocks from low, boundary rows (whose sequences share 16 columns; one row is
-// cheap) as lora_low_kernel has multiplied them by B already.
+// Block queries take them as further k-steps of their unit: weight rows B_a of the sequence's
+// adapter against split[], low as two bf16 parts (high + low: 16 bits of the fp32 sum), into the
+// sequence's accumulator columns only. For that a sequence's block starts at a multiple of 16
+// columns, the MMA's step in N (the rows between are outside the tensor map's block dimension and
+// read as zeros): no adapter's infinities reach another sequence. Boundary rows, whose sequences
+// share 16 columns, are added by the epilogue in fp32; one row is cheap, and lora_low_kernel has
+// multiplied them by B already.
 struct PLora {
   ls_lora bank;
-  float* low;            // [b][L][B][rank], or
-  __nv_bfloat16* split;  // [b][L][2][B][rank], null: low is used
+  __nv_bfloat16* split;  // [b][L][2][pitch][rank]
   float* add;            // [b][L][2 Hkv D]: scale * B (A boundary)
 };
 
@@ -232,7 +233,7 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
   // step(sequence of the tile, adapter, rank chunk of 64) in order until it returns false.
   auto adapter_steps = [&](const PItem& it, const PUnit& u, auto&& step) -> bool {
     if constexpr (kLora) {
-      if (u.p != 0 || !lora.split || it.k1 != a.k_steps) return true;
+      if (u.p != 0 || it.k1 != a.k_steps) return true;
       const PProblem& P = a.pr[0];
       const int seq0 = u.mt * P.seq_per_unit, n = min(P.seq_per_unit, a.b - seq0);
       for (int i = 0; i < n; ++i) {
@@ -300,12 +301,12 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
             allow_dependent_launch();
             waited = true;
           }
-          if (!begin_step(is_a ? uint32_t(kPABytes) : uint32_t(2 * P.rows_per_seq * kPKStep * 2))) return false;
+          if (!begin_step(is_a ? uint32_t(kPABytes) : uint32_t(2 * P.pitch * kPKStep * 2))) return false;
           if (is_a)
             tma_load_2d(a_ring + st * kPABytes, &wl, rc, (ad * a.L + u.l) * P.n_out + u.nt * kPTileN, full);
           else
             tma_load_2d(b_ring + st * kPBBytes, &xl, rc,
-                        ((u.mt * P.seq_per_unit + i) * a.L + u.l) * 2 * P.rows_per_seq, full);
+                        ((u.mt * P.seq_per_unit + i) * a.L + u.l) * 2 * P.pitch, full);
           ++k;
           return true;
         });
@@ -348,8 +349,8 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
             tc_fence_after();
             const uint64_t da = sdesc(smem_u32(a_ring + sa * kPABytes), 16, 1024);
             const uint64_t db = sdesc(smem_u32(b_ring + sb * kPBBytes), 16, 1024);
-            const uint32_t ids = idesc_bf16(P.rows_per_seq, false, kPTileN), ds = d + uint32_t(i * P.rows_per_seq);
-            const uint32_t low_part = uint32_t(P.rows_per_seq * kPKStep * 2 >> 4);
+            const uint32_t ids = idesc_bf16(P.pitch, false, kPTileN), ds = d + uint32_t(i * P.pitch);
+            const uint32_t low_part = uint32_t(P.pitch * kPKStep * 2 >> 4);
 #pragma unroll
             for (int kk = 0; kk < kPKStep / 16; ++kk) {
               if (rc + 16 * kk >= lora.bank.rank) break;
@@ -388,65 +389,20 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
       mbar_arrive(&s.epi);
       return __all_sync(0xffffffffu, pwait(s, &s.epi, uint32_t(meets++) & 1, a.err));
     };
-    // The adapters' part where no further k-steps bring it, for this thread's weight row n and
-    // activation rows col .. col + n - 1: boundary rows have theirs ready, odd blocks get
-    // B[n] . low[row], in fp32 on CUDA cores, beside the next unit's products. Eight rows' loads are
-    // in flight together (a sequence without an adapter reads adapter 0 and leaves its sum out);
-    // low is one address for the whole warp.
-    const int R = lora.bank.rank;
-    auto add_low = [&](const PUnit& u, const PProblem& P, int col, int n, float (&v)[32]) {
-      const int rps = P.rows_per_seq, seq0 = u.mt * P.seq_per_unit;
-      if (u.p) {
-        const float* add = lora.add + (int64_t(seq0 + col) * a.L + u.l) * P.n_out + u.nt * kPTileN + ecol;
+    // the adapters' part of boundary rows col .. col + n - 1, for this thread's weight row
+    auto add_boundary = [&](const PUnit& u, const PProblem& P, int col, int n, float (&v)[32]) {
+      const int sq = u.mt * P.seq_per_unit + col;
+      const float* add = lora.add + (int64_t(sq) * a.L + u.l) * P.n_out + u.nt * kPTileN + ecol;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j >= n) break;
-          const int ad = lora.bank.adapter_of[seq0 + col + j];
-          if (ad >= 0 && ad < lora.bank.n_adapters) v[j] += __ldcg(add + int64_t(j) * a.L * P.n_out);
-        }
-        return;
-      }
-      const __nv_bfloat16* bank = static_cast<const __nv_bfloat16*>(lora.bank.b_q) +
-                                  (int64_t(u.l) * P.n_out + u.nt * kPTileN + ecol) * R;
-#pragma unroll
-      for (int j0 = 0; j0 < 32; j0 += 8) {
-        if (j0 >= n) break;
-        const __nv_bfloat16* w[8];
-        const float* h[8];
-        float x[8];
-        uint32_t has = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int m = col + min(j0 + j, n - 1), sq = seq0 + m / rps;
-          const int ad = lora.bank.adapter_of[sq];
-          const bool one = ad >= 0 && ad < lora.bank.n_adapters;
-          has |= uint32_t(one) << j;
-          w[j] = bank + int64_t(one ? ad : 0) * a.L * P.n_out * R;
-          h[j] = lora.low + ((int64_t(sq) * a.L + u.l) * rps + m % rps) * R;
-          x[j] = 0.f;
-        }
-#pragma unroll 1
-        for (int e = 0; e < R; e += 8) {
-          uint4 wv[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) wv[j] = ld_nc_v4(w[j] + e);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float f[8];
-            Elem<__nv_bfloat16>::to_f32(wv[j], f);
-            const float4 p = __ldg(reinterpret_cast<const float4*>(h[j] + e)), q = __ldg(reinterpret_cast<const float4*>(h[j] + e) + 1);
-            x[j] += fmaf(f[3], p.w, fmaf(f[2], p.z, fmaf(f[1], p.y, f[0] * p.x))) +
-                    fmaf(f[7], q.w, fmaf(f[6], q.z, fmaf(f[5], q.y, f[4] * q.x)));
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if ((has >> j) & 1) v[j0 + j] += x[j];
+      for (int j = 0; j < 32; ++j) {
+        if (j >= n) break;
+        const int ad = lora.bank.adapter_of[sq + j];
+        if (ad >= 0 && ad < lora.bank.n_adapters) v[j] += __ldcg(add + int64_t(j) * a.L * P.n_out);
       }
     };
     auto store_tile = [&](const PUnit& u, const PProblem& P, auto&& fetch) -> bool {
       const int seq0 = u.mt * P.seq_per_unit;
-      const int rows = min(P.seq_per_unit, a.b - seq0) * P.rows_per_seq;  // valid activation rows
+      const int rows = min(P.seq_per_unit, a.b - seq0) * P.pitch;  // activation rows of the tile
       for (int r0 = 0; r0 < rows; r0 += kPOutRows, ++pass) {
         // the staging tile is free once every thread has copied the previous pass out
         if (pass > 0 && !__all_sync(0xffffffffu, pwait(s, &s.out_free, (pass - 1) & 1, a.err))) return false;
@@ -455,7 +411,7 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
           float v[32];
           fetch(r0 + c0, v);
           if constexpr (kLora) {
-            if ((u.p || !lora.split) && r0 + c0 < rows) add_low(u, P, r0 + c0, min(32, rows - r0 - c0), v);
+            if (u.p && r0 + c0 < rows) add_boundary(u, P, r0 + c0, min(32, rows - r0 - c0), v);
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) stage[(c0 + j) * kPTileN + ecol] = __float2bfloat16_rn(v[j]);
@@ -465,7 +421,8 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
         const int vr = min(kPOutRows, rows - r0);
         for (int c = etid; c < vr * 16; c += 128) {  // 16 pieces of 16 bytes per row
           const int m = r0 + (c >> 4);
-          const int sq = seq0 + m / P.rows_per_seq, r = m % P.rows_per_seq;
+          const int sq = seq0 + m / P.pitch, r = m % P.pitch;
+          if (r >= P.rows_per_seq) continue;
           uint4* dst = reinterpret_cast<uint4*>(P.y + ((int64_t(sq) * a.L + u.l) * P.rows_per_seq + r) * P.n_out +
                                                 u.nt * kPTileN) + (c & 15);
           *dst = reinterpret_cast<const uint4*>(stage + (c >> 4) * kPTileN)[c & 15];
@@ -604,8 +561,8 @@ __global__ void __launch_bounds__(low_warps(NT) * 32) lora_low_kernel(const __gr
 #pragma unroll
   for (int m = 0; m < 2 * MT; ++m) xr[m] = src + int64_t(min(m * 8 + g, rows - 1)) * hidden;
   const float scale = lora.bank.scale[ad];
-  __nv_bfloat16* split = lora.split + (int64_t(b) * L + l) * 2 * B * R;
-  float* low = lora.low + (int64_t(b) * L + l) * B * R;
+  const int pitch = (B + 15) & ~15;  // (rows past the block feed columns that are not stored)
+  __nv_bfloat16* split = lora.split + (int64_t(b) * L + l) * 2 * pitch * R;
   for (int r0 = p ? 0 : int(blockIdx.y) * 8 * NT; r0 < R; r0 += 8 * NT) {
     const int nr = min(8 * NT, R - r0);
     const __nv_bfloat16* wr[NT];
@@ -656,13 +613,11 @@ __global__ void __launch_bounds__(low_warps(NT) * 32) lora_low_kernel(const __gr
         sum *= scale;
         if (p) {
           low_s[r0 + r] = sum;
-        } else if (lora.split) {
+        } else {
           const __nv_bfloat16 hi = __float2bfloat16_rn(sum);
           const float rest = sum - __bfloat162float(hi);
           split[row * R + r0 + r] = hi;
-          split[(B + row) * R + r0 + r] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.f);  // (an infinite sum stays infinite)
-        } else {
-          low[row * R + r0 + r] = sum;
+          split[(pitch + row) * R + r0 + r] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.f);  // (an infinite sum stays infinite)
         }
       }
       __syncthreads();
@@ -699,9 +654,9 @@ bool encode_bf16(void* base, int rank, const cuuint64_t* dims, const cuuint64_t*
 bool prologue_supported(const Dev& p) { return prologue_shapes_ok(p.dtype, p.hidden, p.Hq, p.Hkv, p.D, p.B); }
 
 size_t lora_workspace_bytes(const ls_config& c, int rank) {
-  // low (or split) of the block rows, then the boundary rows' finished sums
+  // the block rows' inner products, then the boundary rows' finished sums
   const int64_t bl = int64_t(c.batch) * c.n_layers;
-  return size_t(align256(bl * c.block * rank * 4) + align256(bl * 2 * c.n_kv_heads * c.head_dim * 4));
+  return size_t(align256(bl * ((c.block + 15) & ~15) * rank * 4) + align256(bl * 2 * c.n_kv_heads * c.head_dim * 4));
 }
 
 cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, const void* x, const ls_lora* lora,
@@ -720,8 +675,9 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
   PProblem& Q = a.pr[0];
   Q.n_out = p.Hq * p.D;
   Q.rows_per_seq = p.B;
-  Q.seq_per_unit = kPMaxAct / p.B < p.b ? kPMaxAct / p.B : p.b;
-  Q.load_rows = Q.seq_per_unit * p.B;
+  Q.pitch = lora ? (p.B + 15) & ~15 : p.B;
+  Q.seq_per_unit = kPMaxAct / Q.pitch < p.b ? kPMaxAct / Q.pitch : p.b;
+  Q.load_rows = Q.seq_per_unit * Q.pitch;
   Q.act_rows = (Q.load_rows + 15) & ~15;
   Q.m_tiles = (p.b + Q.seq_per_unit - 1) / Q.seq_per_unit;
   Q.n_units = p.L * (Q.n_out / kPTileN) * Q.m_tiles;
@@ -730,7 +686,7 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
   // problem 1: boundary keys/values, X = the state's boundary view [b][L][hidden]
   PProblem& K = a.pr[1];
   K.n_out = 2 * p.Hkv * p.D;
-  K.rows_per_seq = 1;
+  K.rows_per_seq = K.pitch = 1;
   K.seq_per_unit = p.b < kPMaxAct ? p.b : kPMaxAct;
   K.load_rows = K.seq_per_unit;
   K.act_rows = (K.load_rows + 15) & ~15;
@@ -750,7 +706,7 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
   {
     const cuuint64_t dims[4] = {cuuint64_t(p.hidden), cuuint64_t(p.B), cuuint64_t(p.L), cuuint64_t(p.b)};
     const cuuint64_t str[3] = {hb, hb * p.B, hb * p.B * p.L};
-    const cuuint32_t box[4] = {kPKStep, cuuint32_t(p.B), 1, cuuint32_t(Q.seq_per_unit)};
+    const cuuint32_t box[4] = {kPKStep, cuuint32_t(Q.pitch), 1, cuuint32_t(Q.seq_per_unit)};
     if (!encode_bf16(const_cast<void*>(x), 4, dims, str, box, &mx0)) return cudaErrorInvalidValue;
   }
   {
@@ -770,20 +726,17 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
   CUtensorMap mwl = mw0, mxl = mx0;  // (unused without adapters)
   if (lora) {
     pl.bank = *lora;
-    pl.low = static_cast<float*>(low);
-    pl.add = reinterpret_cast<float*>(static_cast<char*>(low) + align256(int64_t(p.b) * p.L * p.B * lora->rank * 4));
-    if (p.B % 16 == 0) {
-      // the tiles' inner extent is 64 of the rank; what lies past it reads as zeros
-      pl.split = static_cast<__nv_bfloat16*>(low);  // (two bf16 parts in the place of fp32 sums)
-      const cuuint64_t rb = cuuint64_t(lora->rank) * 2;
-      const int64_t w_rows = int64_t(lora->n_adapters) * p.L * Q.n_out, x_rows = int64_t(p.b) * p.L * 2 * p.B;
-      if (w_rows > INT32_MAX || x_rows > INT32_MAX) return cudaErrorNotSupported;
-      const cuuint64_t wd[2] = {cuuint64_t(lora->rank), cuuint64_t(w_rows)}, xd[2] = {cuuint64_t(lora->rank), cuuint64_t(x_rows)};
-      const cuuint64_t str[1] = {rb};
-      const cuuint32_t wbox[2] = {kPKStep, kPTileN}, xbox[2] = {kPKStep, cuuint32_t(2 * p.B)};
-      if (!encode_bf16(const_cast<void*>(lora->b_q), 2, wd, str, wbox, &mwl)) return cudaErrorInvalidValue;
-      if (!encode_bf16(low, 2, xd, str, xbox, &mxl)) return cudaErrorInvalidValue;
-    }
+    pl.split = static_cast<__nv_bfloat16*>(low);
+    pl.add = reinterpret_cast<float*>(static_cast<char*>(low) + align256(int64_t(p.b) * p.L * Q.pitch * lora->rank * 4));
+    // the tiles' inner extent is 64 of the rank; what lies past it reads as zeros
+    const cuuint64_t rb = cuuint64_t(lora->rank) * 2;
+    const int64_t w_rows = int64_t(lora->n_adapters) * p.L * Q.n_out, x_rows = int64_t(p.b) * p.L * 2 * Q.pitch;
+    if (w_rows > INT32_MAX || x_rows > INT32_MAX) return cudaErrorNotSupported;
+    const cuuint64_t wd[2] = {cuuint64_t(lora->rank), cuuint64_t(w_rows)}, xd[2] = {cuuint64_t(lora->rank), cuuint64_t(x_rows)};
+    const cuuint64_t str[1] = {rb};
+    const cuuint32_t wbox[2] = {kPKStep, kPTileN}, xbox[2] = {kPKStep, cuuint32_t(2 * Q.pitch)};
+    if (!encode_bf16(const_cast<void*>(lora->b_q), 2, wd, str, wbox, &mwl)) return cudaErrorInvalidValue;
+    if (!encode_bf16(low, 2, xd, str, xbox, &mxl)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t lc{};
     const int tiles = lora->rank <= 8 ? 1 : (lora->rank <= 16 ? 2 : 4);  // (x is read again for each 32 of the rank)
     lc.gridDim = dim3(p.b * p.L, (lora->rank + 8 * tiles - 1) / (8 * tiles) + 1);
