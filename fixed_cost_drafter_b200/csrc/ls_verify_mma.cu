@@ -1,8 +1,10 @@
 // ls_verify_attend_kv4 for few query rows per KV head (decoding, short blocks) of bf16 states.
 //
-// What bounds it: reading the cache. At one row per sequence every byte of the cache is used
-// for 4 rows x 2 flops an element, so the kernel's work is to turn 4-bit codes into fp16 MMA
-// operands as fast as the bytes arrive. The operands are made in registers, from shared
+// Measured: decoding 16 requests at 48K-64K tokens, 1.06 GB of cache: 230 us, 4.6 TB/s (70 % of
+// the copy rate). The work is to turn 4-bit codes into fp16 MMA operands as fast as the bytes
+// arrive: about 2200 warp instructions per 128 keys, half of them conversions and scalings, at
+// 0.57 a cycle and sub-partition bound it (four CTAs per SM with two stages each, 96 registers:
+// the same; five: 295 us). The operands are made in registers, from shared
 // memory that bulk copies fill (a page's block of one KV head is one contiguous copy), and
 // never go back to shared memory: warp-level m16n8k16 products, whose M = 16 side is the
 // cache (16 keys, then 16 output dimensions) and whose N = 8 side the query rows.

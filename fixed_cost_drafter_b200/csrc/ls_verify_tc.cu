@@ -1,35 +1,36 @@
 // ls_verify_attend_kv4 for many query rows per KV head (a verification pass's B + 1 rows of a
 // GQA group) of bf16 states, on the 5th-generation tensor cores.
 //
-// What bounds it: at 68 rows the two products (128 rows x 128 keys x D each, tcgen05 f16) take
-// about as long as the bytes of the cache take to arrive, and the operands have to be made
-// first: shared memory carries every fp16 operand twice (written by the conversion, read by
-// the MMA). So what can stays out of it: Q and the weights P are the MMAs' A operands in TMEM.
-// The codes do go through it, as bulk copies: loaded straight into the converting threads'
-// registers, two units of 16 rows ahead, every use of a loaded value waited for the newest
-// loads as well (about 3000 cycles a unit).
+// Measured: 16 requests x 17 rows (68 rows per KV head) at 32K-64K tokens, 906 MB of cache: 470 to
+// 525 us over runs (1.8 TB/s), 13.9 ms on CUDA cores. What bounds it: instructions and the
+// latencies between roles. The two products of a 128-key chunk (128 rows x 128 keys x D each)
+// need 1024 cycles, its bytes about 760 at the copy rate, its weights' exponentials 1024 (68 rows
+// fill the lanes of three SM sub-partitions); a chunk takes about 2500, for some 4500 warp
+// instructions at 0.45 a cycle and sub-partition. A wait for a barrier costs about 200 cycles
+// even when its phase is complete, so each role takes large steps. Tried without gain: a third
+// softmax group with its own S buffer, four groups of half-chunks, 28 and 32 warps (fewer
+// registers, more instructions), codes fetched by the converting threads themselves (into
+// registers or with cp.async: every later fence or load waits for them).
 //
-// One CTA per SM, 16 warps; the roles meet at mbarriers:
-//   warp 10     producer: a chunk's pages into a ring of 4 stages (the page's block of a KV head
-//               is one copy)
-//   warps 11-15 conversion, with the softmax warps that have no rows (68 rows leave two idle, in
+// One CTA per SM, 20 warps; the roles meet at mbarriers:
+//   warp 10     producer: a chunk's pages into a ring of 3 stages (ls_verify.cuh)
+//   warps 11-19 conversion, with the softmax warps that have no rows (68 rows leave two idle, in
 //               the SM sub-partition that then has no softmax at all): tasks of 32 rows of a
 //               chunk's K or V, round robin, a thread 16 codes (one scale group) at a time; tiles
 //               in the 128-byte swizzle, two buffers each. A group's two 16-byte pieces go to
 //               different 64-column halves (D = 128), so that eight threads fill a whole 128-byte
 //               row; Q and the output columns follow the same order.
-//   warp 8      S = Q K^T of a chunk into one of two 128-column buffers (8 MMAs of N = 128: an
-//               MMA costs its issuing thread about 80 cycles whatever its N)
-//   warps 0-7   softmax, a thread per query row, 64 keys at a time: weights 2^(x - r) in fp16,
-//               written over S. The reference r only moves when 64 weights sum to more than
-//               2^15 (fp16 holds up to 65504); it is then the maximum less 8, as in
-//               ls_verify_mma.cu, and the row of O is scaled in TMEM. The sum is needed anyway:
-//               the check costs no maximum. Warps 0-3 take the even chunks, 4-7 the odd ones
-//               (a lone warp per SM sub-partition waits out every latency: 522 us instead of
-//               the figure below); one O needs one reference, so a warp passes it on with each
-//               chunk and takes the other's up before it writes its weights.
-//   warp 9      O += P V, 64 keys at a time
-// TMEM columns: S / P 0-255, O 256-383, Q 384-447.
+//   warp 8      S = Q K^T of a chunk into one of two 128-column buffers
+//   warps 0-7   softmax, a thread per query row, 64 keys at a time: weights 2^(x - r) in fp16. The
+//               reference r only moves when 64 weights sum to more than 2^15 (fp16 holds up to
+//               65504); it is then the maximum less 8, as in ls_verify_mma.cu, and the row of O is
+//               scaled in TMEM. The sum is needed anyway: the check costs no maximum. Warps 0-3
+//               take the even chunks, 4-7 the odd ones; one O needs one reference, so a group
+//               passes it on with each chunk (a counter in shared memory) and takes the other's
+//               up before it hands its weights over.
+//   warp 9      O += P V, 64 keys at a time, P the MMA's A operand in TMEM. (P over S instead held
+//               each S buffer until its P V was done: 513 us.)
+// TMEM columns: S 0-255, O 256-383, P 384-511.
 // Rounding, exactness of the held values and NaN groups: as in ls_verify_mma.cu.
 #include "ls_verify.cuh"
 #include "ls_tc.cuh"

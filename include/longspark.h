@@ -136,7 +136,8 @@ typedef struct {
  *   counters  int64 [b][L][1 + n_scales]: retained length len, then for each scale the
  *             number of segments finalised so far (floor(len / s_k)).
  *   error     int32 [4]: word 0 is the device error word.
- *   sync      int32 [b][L]: zero between calls (arrival counts inside a commit).
+ *   sync      int32 [b][L]: zero between calls (arrival counts inside a commit, and inside
+ *             ls_pages_extend / ls_pages_trim).
  *   kv        e     [b][L][Hkv][2][kv_rows][D]: for K (index 0) and V (index 1) of each
  *             (sequence, layer, KV head) tile, rows 0..W-1 are the ring window, then for
  *             each scale k rows W + k*(slots+1) + i hold the mean of the segment in slot i
@@ -524,11 +525,14 @@ LS_API size_t ls_verify_workspace_bytes(const ls_config* cfg, int32_t n_rows);
  *               that may overlap on the GPU (two streams, two graphs) need one each.
  * n_rows <= B + 1. A kv_len outside [0, max_blocks * page_size] sets LS_DEVERR_PREFIX_LEN and
  * counts as 0; a row count outside [0, n_rows] sets LS_DEVERR_ROWS and is clamped; a page id
- * outside [0, num_pages) sets LS_DEVERR_PAGE and is read as page 0. What lies in the cache
- * behind kv_len (stale rows, NaN scales) does not reach the output. bf16 states run on the
- * tensor cores: keys and values are exact there, queries and softmax weights are rounded to
- * fp16 (11 bits; queries after scaling each row to a largest element near 1); fp32 states
- * run in fp32 on CUDA cores. Repeated calls give the same bits.                           */
+ * outside [0, num_pages) sets LS_DEVERR_PAGE and is read as page 0. What a query row does not
+ * see (rows behind its own, stale rows behind kv_len, NaN scales among them) does not reach
+ * its output; a value group with a NaN scale that it does see makes the group's 16 outputs NaN,
+ * a key's the whole head's. bf16 states run on the tensor cores (up to 24 query rows per KV head
+ * with warp-level products, more with tcgen05): keys and values are exact there, queries and
+ * softmax weights are rounded to fp16 (11 bits; queries after scaling each row to a largest
+ * element near 1). fp32 states, and bf16 ones with LS_FLAG_FORCE_SIMT, run in fp32 on CUDA
+ * cores. Repeated calls give the same bits.                                               */
 LS_API int ls_verify_attend_kv4(const ls_state* st, const ls_paged_kv4* h_kv, int32_t layer, const void* d_q,
                                 int64_t q_stride, int32_t n_rows, const int32_t* d_rows, const int64_t* d_kv_len,
                                 float softmax_scale, void* d_out, void* d_workspace, size_t workspace_bytes,
@@ -559,8 +563,9 @@ LS_API size_t ls_lora_workspace_bytes(const ls_config* cfg, int32_t rank);
 /* ls_draft_prologue with sequence b's adapter a = adapter_of[b] added to both projections:
  *   q[b][l][i]  = W_q[l]  x[b][l][i]      + scale[a] B_q[a][l]  (A_q[a][l]  x[b][l][i])
  *   bkv[b][l]   = W_kv[l] boundary[b][l]  + scale[a] B_kv[a][l] (A_kv[a][l] boundary[b][l])
- * summed in fp32 and rounded to bf16 once. The sum over the rank is taken apart from the one
- * over the hidden size; a sequence without an adapter gets what ls_draft_prologue gives it,
+ * summed in fp32 and rounded to bf16 once; the block queries' inner sums scale A x are held in
+ * two bf16 parts (16 bits) between their products. The sum over the rank is taken apart from the
+ * one over the hidden size; a sequence without an adapter gets what ls_draft_prologue gives it,
  * and nothing of one sequence's adapter reaches another's rows. An id outside
  * [-1, n_adapters) sets LS_DEVERR_ADAPTER and counts as -1. Arguments, limits and launch
  * rules as ls_draft_prologue; the adapters' weights and adapter_of may be written by the
