@@ -264,6 +264,9 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
         codes[x] = blk + off * (D / 2) + g * 8;
         scales[x] = blk + ps * D + off * kGroups + g;
       }
+      // (the tile first: the products two chunks back are done, so the stage's phase before this
+      // one, three chunks back, is complete, and the parity names this one)
+      if (chunk >= 2 && !ver_wait_warp(s, &empty[st], uint32_t((chunk >> 1) - 1) & 1, a.err)) break;
       if (!ver_wait_warp(s, &s.raw_full[rs], uint32_t(chunk / kTRing) & 1, a.err)) break;
       uint2 w[kIter];
       uint32_t sc[kIter];
@@ -272,7 +275,6 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
         w[i] = *reinterpret_cast<const uint2*>(codes[i / (kIter / 2)] + (i % (kIter / 2)) * kRowStep * (D / 2));
         sc[i] = scales[i / (kIter / 2)][(i % (kIter / 2)) * kRowStep * kGroups];
       }
-      if (chunk >= 2 && !ver_wait_warp(s, &empty[st], uint32_t((chunk >> 1) - 1) & 1, a.err)) break;
       if (v) {
         bool nan = false;
 #pragma unroll
