@@ -144,13 +144,16 @@ int validate_paged(const ls_config& c, const ls_paged_kv* kv) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+constexpr int32_t kMostRows = 1 << 30;
+
 int validate_pool(const ls_page_pool* pool) {
   if (!pool || !pool->block_table || !pool->held || !pool->free_pages || !pool->free_count) return LS_ERR_INVALID_ARG;
   if (!aligned(pool->block_table, 4) || !aligned(pool->held, 4) || !aligned(pool->free_pages, 4) ||
       !aligned(pool->free_count, 4))
     return LS_ERR_INVALID_ARG;
   if (pool->max_blocks < 1 || pool->page_size < 1 || pool->num_pages < 1) return LS_ERR_INVALID_ARG;
-  return pool->num_pages > INT32_MAX ? LS_ERR_UNSUPPORTED : LS_OK;
+  // (page ids are int32; 32-bit counts of entries and rows with room for a step past the end)
+  return pool->num_pages > INT32_MAX || pool->max_blocks > kMostRows ? LS_ERR_UNSUPPORTED : LS_OK;
 }
 
 bool kv4_shapes_ok(const ls_config& c, int page_size) {
@@ -505,6 +508,7 @@ int ls_pages_extend(ls_state* st, const ls_page_pool* h_pool, const int64_t* d_l
   if (slot_capacity > 0 && !d_slots) return LS_ERR_INVALID_ARG;
   if (!aligned(d_len, 8) || !aligned(d_rows, 4) || !aligned(d_row_begin, 8) || !aligned(d_slots, 8))
     return LS_ERR_INVALID_ARG;
+  if (max_rows > kMostRows) return LS_ERR_UNSUPPORTED;
   if (!d_row_begin && slot_capacity < int64_t(st->cfg.batch) * max_rows) return LS_ERR_SHAPE;
   const int r = cuda_status(ls::launch_pages_extend(st->dev, *h_pool, d_len, d_rows, max_rows, d_row_begin, d_slots,
                                                     slot_capacity, st->sms, stream));

@@ -415,7 +415,8 @@ LS_API int ls_round_paged(ls_state* st, const int32_t* d_draft_ids, const int32_
  *   held        int32 [b]: pages each sequence holds.
  *   free_pages  int32 [num_pages]: a stack; entries [0, *free_count) are the free pages.
  *   free_count  int32 [1].
- *   page_size   rows per page, any size >= 1.                                           */
+ *   page_size   rows per page, any size >= 1.
+ * max_blocks <= 2^30, num_pages < 2^31 (else LS_ERR_UNSUPPORTED).                        */
 typedef struct {
   int32_t* block_table;
   int32_t* held;
@@ -430,7 +431,8 @@ typedef struct {
  * (page * page_size + offset; an engine's slot mapping, ls_paged_kv.verify_slots).
  *   d_len        int64 [b]: rows sequence b holds (its next row is at position len), or
  *                NULL: the lengths the state itself holds (after its commits).
- *   d_rows       int32 [b]: new rows of sequence b, 0 .. max_rows, or NULL: max_rows each.
+ *   d_rows       int32 [b]: new rows of sequence b, 0 .. max_rows, or NULL: max_rows each
+ *                (max_rows <= 2^30, else LS_ERR_UNSUPPORTED).
  *   d_row_begin  NULL: d_slots is [b][max_rows]; entries past a sequence's rows get -1.
  *                Else int64 [b+1] out: the running sum of the row counts; sequence b's slots
  *                are d_slots[row_begin[b] .. row_begin[b+1]), and entries past the last

@@ -226,6 +226,8 @@ def test_refusals():
         refused(bad, F.ls_pages_extend, lib.st, desc, None, None, 4, None, s, 8)
         refused(bad, F.ls_pages_trim, lib.st, desc, None)
     refused(F.LS_ERR_UNSUPPORTED, F.ls_pages_trim, lib.st, F.make_page_pool(*p, 4, 16, 1 << 31), None)
+    refused(F.LS_ERR_UNSUPPORTED, F.ls_pages_trim, lib.st, F.make_page_pool(*p, (1 << 30) + 1, 16, 8), None)
+    refused(F.LS_ERR_UNSUPPORTED, F.ls_pages_extend, lib.st, pool.desc, None, None, (1 << 30) + 1, s, s, 1 << 40)
     refused(F.LS_ERR_SHAPE, F.ls_pages_extend, lib.st, pool.desc, None, None, 4, None, s, 7)
     refused(bad, F.ls_pages_extend, lib.st, pool.desc, None, None, -1, None, s, 8)
     refused(bad, F.ls_pages_extend, lib.st, pool.desc, None, None, 4, None, None, 8)
