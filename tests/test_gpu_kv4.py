@@ -188,7 +188,8 @@ def _check(lib, cache, lengths, q, out, rows, n, scale=None):
 
 SHAPES = {  # kv_heads, q_heads, dim, block
     "qwen3": (8, 32, 128, 16), "mid": (2, 8, 128, 16), "narrow": (4, 16, 64, 16), "mha": (3, 3, 128, 16),
-    "pair": (2, 4, 128, 32), "mqa": (1, 24, 64, 2), "wide": (2, 40, 128, 3), "most": (1, 64, 64, 1)}
+    "pair": (2, 4, 128, 32), "mqa": (1, 24, 64, 2), "wide": (2, 40, 128, 3), "most": (1, 64, 64, 1),
+    "seven": (1, 7, 128, 9), "odd": (1, 55, 64, 1)}
 
 
 @pytest.mark.parametrize("shape,dtype,flags,ps,n,lengths", [
@@ -215,6 +216,14 @@ SHAPES = {  # kv_heads, q_heads, dim, block
     ("most", "bf16", 0, 16, 1, [700]),
     ("wide", "bf16", 0, 16, 4, [9, 600]),
     ("mid", "bf16", 0, 16, 3, [130] * 70),
+    ("mid", "bf16", 0, 16, 7, [7, 300, 1, 1025]),
+    ("mid", "bf16", 0, 16, 8, [2000, 8]),
+    ("seven", "bf16", 0, 32, 4, [4, 260, 901]),
+    ("seven", "bf16", 2, 16, 10, [17, 3, 800]),
+    ("odd", "bf16", 0, 16, 2, [2, 1, 900]),
+    ("odd", "bf16", 2, 64, 1, [300]),
+    ("seven", "bf16", 0, 16, 3, [129, 700]),
+    ("mid", "bf16", 0, 16, 17, [20 + i % 150 for i in range(200)]),
 ])
 def test_attention(shape, dtype, flags, ps, n, lengths):
     kvh, qh, D, block = SHAPES[shape]
@@ -223,6 +232,40 @@ def test_attention(shape, dtype, flags, ps, n, lengths):
     q, out = _attend(lib, cache, lengths, n, q_extra=8 * n)
     _check(lib, cache, lengths, q, out, None, n)
     assert lib.error() == (F.LS_OK, 0)
+
+
+@pytest.mark.parametrize("shape,n", [("qwen3", 17), ("qwen3", 1), ("qwen3", 7), ("narrow", 17), ("narrow", 1)])
+def test_long_lists_of_shared_pages(shape, n):
+    """Twenty steps of 128 keys and more per CTA; pages that several blocks and sequences name."""
+    kvh, qh, D, block = SHAPES[shape]
+    lib = Lib(batch=3, kv_heads=kvh, q_heads=qh, dim=D, block=block)
+    cache = Cache4(lib, [64 * 16, 0, 0], 16, seed=21)
+    lengths = [24000, 9001, 18333] if D == 128 else [48000, 18001, 36333]
+    cache.mb = -(-max(lengths) // 16)
+    cache.table = np.random.default_rng(n).integers(0, cache.pages, (3, cache.mb), dtype=np.int32)
+    cache.upload()
+    q, out = _attend(lib, cache, lengths, n)
+    assert lib.error() == (F.LS_OK, 0)
+    # the formula in 64 bits, all rows of a KV head at once; each page decoded once
+    held = [np.zeros((cache.pages, 16, kvh, D)) for _ in range(2)]
+    for p in range(cache.pages):
+        for h in range(kvh):
+            kc, vc, ks, vs = cache.sections(p, h)
+            held[0][p, :, h], held[1][p, :, h] = O.kv4_decode(kc, ks), O.kv4_decode(vc, vs)
+    grp, scale = qh // kvh, D ** -0.5
+    for b, t in enumerate(lengths):
+        k, v = (torch.from_numpy(x[cache.table[b]].reshape(-1, kvh, D)[:t]).cuda() for x in held)
+        seen = torch.arange(t, device="cuda") <= torch.arange(t - n, t, device="cuda")[:, None]
+        for h in range(kvh):
+            qs = q[b].double().view(n, qh, D)[:, h * grp:(h + 1) * grp]
+            x = (scale * (qs @ k[:, h].T)).masked_fill(~seen[:, None], -torch.inf)
+            w = torch.softmax(x, -1)
+            ref, mass = w @ v[:, h], w @ v[:, h].abs()
+            dot = (qs.abs() @ k[:, h].abs().T).amax(-1, keepdim=True)
+            ex = (D + 8) * 2.0 ** -24 * scale * dot + D * 2.0 ** -25 * scale * qs.abs().amax(-1, keepdim=True) * k[:, h].abs().max()
+            tol = 2.0 ** -8 * ref.abs() + (2.0 ** -10 + 2 * ex + 2 * (t + 256) * 2.0 ** -24) * mass + t * 2.0 ** -33 * v[:, h].abs().max()
+            exc = (out[b, :, h * grp:(h + 1) * grp].double() - ref).abs() - tol
+            assert exc.max() <= 0, (b, h, float(exc.max()))
 
 
 @pytest.mark.parametrize("shape,n,dtype", [("mid", 17, "bf16"), ("mid", 5, "bf16"), ("narrow", 17, "bf16"), ("narrow", 5, "f32")])
