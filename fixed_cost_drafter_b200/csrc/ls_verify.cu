@@ -207,18 +207,21 @@ __global__ void __launch_bounds__(kVThreads) verify_join_kernel(const VerArgs a)
   }
   const int r = int(blockIdx.y) * (kVThreads / 32) + warp;
   const int i = (m0 + r) / a.grp, j = (m0 + r) - i * a.grp;
-  if (r >= a.MR || m0 + r >= a.M || i >= rows) return;
+  bool mine = r < a.MR && m0 + r < a.M && i < rows;
   int c_first = 0, c_last = -1;
-  if (n > 0) {  // the CTAs whose ranges hold the tile's first and last chunk
+  if (mine && n > 0) {  // the CTAs whose ranges hold the tile's first and last chunk
     const int64_t T = ver_chunks_before(a, a.b) * a.HM, t0 = ver_chunks_before(a, b) * a.HM + hm * n;
     const int64_t G = T < a.G ? T : a.G;
     c_first = int(((t0 + 1) * G + T - 1) / T) - 1;
     c_last = int(((t0 + n) * G + T - 1) / T) - 1;
-    if (c_first == c_last) return;  // the tile's CTA has written it
+    mine = c_first != c_last;  // else the tile's CTA has written it
   }
+  // Every thread waits, those without a row too: what is launched next waits for this grid only,
+  // and this grid must not be complete before the one whose output it stands for.
+  grid_dependency_wait();
+  if (!mine) return;
   // the first piece starts its tile (an odd slot), the others start their CTAs' ranges
   auto at = [&](int c) { return (int64_t(2 * c) + (c == c_first ? 1 : 0)) * a.MR + r; };
-  grid_dependency_wait();
   float o[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) o[e] = 0.f;

@@ -430,6 +430,33 @@ def test_two_streams_and_captured_calls():
     assert lib.error() == (F.LS_OK, 0)
 
 
+@pytest.mark.parametrize("n", [1, 17])
+def test_a_call_after_it_sees_the_whole_output(n):
+    """Short sequences: no tile is cut, so the joining kernel has no work, and the next call of the
+    library (which may be scheduled early) reads the output all the same."""
+    b = 64
+    lib = Lib(batch=b, kv_heads=2, q_heads=2, block=16)
+    lengths = [17 + i for i in range(b)]
+    cache = Cache4(lib, lengths, 16, seed=14)
+    q, want = _attend(lib, cache, lengths, n)
+    t = torch.tensor(lengths, dtype=torch.int64, device="cuda")
+    ws = torch.empty(F.ls_verify_workspace_bytes(lib.cfg, n), dtype=torch.uint8, device="cuda")
+    rows = b * n
+    slots = torch.arange(rows, dtype=torch.int64, device="cuda")
+    dst = torch.zeros(2, -(-rows // 16), F.ls_kv4_page_bytes(lib.cfg, 16), dtype=torch.uint8, device="cuda")
+    held = [F.make_paged_kv4([x], x.stride(0), None, 1, 16, x.shape[0]) for x in dst]
+    F.ls_kv4_append(lib.st, held[0], 0, want, want, 256, slots, rows)
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    for _ in range(50):
+        out.zero_()
+        dst[1].zero_()
+        F.ls_verify_attend_kv4(lib.st, cache.kv, 0, q, q.stride(1), n, None, t, 128 ** -0.5, out, ws, ws.numel())
+        F.ls_kv4_append(lib.st, held[1], 0, out, out, 256, slots, rows)
+        assert torch.equal(dst[0], dst[1])
+    assert lib.error() == (F.LS_OK, 0)
+
+
 def test_refusals():
     lib = Lib(batch=2, layers=2)
     cache = Cache4(lib, [20, 30], 16)
