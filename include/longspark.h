@@ -416,6 +416,7 @@ LS_API int ls_round_paged(ls_state* st, const int32_t* d_draft_ids, const int32_
  *   free_pages  int32 [num_pages]: a stack; entries [0, *free_count) are the free pages.
  *   free_count  int32 [1].
  *   page_size   rows per page, any size >= 1.
+ * A page belongs to one sequence: one that two block tables name is returned by each.
  * max_blocks <= 2^30, num_pages < 2^31 (else LS_ERR_UNSUPPORTED).                        */
 typedef struct {
   int32_t* block_table;
@@ -567,8 +568,9 @@ LS_API size_t ls_lora_workspace_bytes(const ls_config* cfg, int32_t rank);
  *   bkv[b][l]   = W_kv[l] boundary[b][l]  + scale[a] B_kv[a][l] (A_kv[a][l] boundary[b][l])
  * summed in fp32 and rounded to bf16 once; the block queries' inner sums scale A x are held in
  * two bf16 parts (16 bits) between their products. The sum over the rank is taken apart from the
- * one over the hidden size; a sequence without an adapter gets what ls_draft_prologue gives it,
- * and nothing of one sequence's adapter reaches another's rows. An id outside
+ * one over the hidden size; a sequence without an adapter gets what ls_draft_prologue gives it
+ * (the sums over the hidden size may be split in other places where B is no multiple of 16), and
+ * nothing of one sequence's adapter reaches another's rows. An id outside
  * [-1, n_adapters) sets LS_DEVERR_ADAPTER and counts as -1. Arguments, limits and launch
  * rules as ls_draft_prologue; the adapters' weights and adapter_of may be written by the
  * kernel launched just before. d_workspace: >= ls_lora_workspace_bytes bytes, 256-byte
