@@ -32,6 +32,8 @@
 // commit writes the boundary view) are read only after the grid dependency wait. Every
 // thread triggers this grid's dependents once it has passed that wait.
 // Every wait is bounded.
+#include <type_traits>
+
 #include "ls_tc.cuh"
 
 namespace ls {
@@ -111,11 +113,13 @@ __device__ inline PUnit unit_of(const PArgs& a, int u) {
   PUnit r;
   r.p = u < a.pr[0].n_units ? 0 : 1;
   if (r.p) u -= a.pr[0].n_units;
-  const int nts = a.pr[r.p].n_out / kPTileN;
+  // activation tiles first: the CTAs that run together share a weight tile, which then comes from
+  // HBM once (64 requests: 4 tiles)
+  const int mts = a.pr[r.p].m_tiles, nts = a.pr[r.p].n_out / kPTileN;
+  r.mt = u % mts;
+  u /= mts;
   r.nt = u % nts;
-  u /= nts;
-  r.l = u % a.L;
-  r.mt = u / a.L;
+  r.l = u / nts;
   return r;
 }
 
@@ -185,6 +189,11 @@ __device__ inline bool pwait(PBars& s, uint64_t* bar, uint32_t parity, int32_t* 
   return false;
 }
 
+// The same by a whole warp.
+__device__ inline bool pwait_warp(PBars& s, uint64_t* bar, uint32_t parity, int32_t* err) {
+  return __all_sync(0xffffffffu, pwait(s, bar, parity, err));
+}
+
 template <bool kLora>
 __global__ void __launch_bounds__(kPThreads, 1)
 prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora lora, const __grid_constant__ CUtensorMap w0, const __grid_constant__ CUtensorMap x0,
@@ -224,21 +233,22 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
   // With adapters the kernel before is lora_low_kernel, which lets this one start once everything
   // before it has completed: only what it writes itself is waited for, by the epilogue (at its
   // start) and by the producers before their first adapter step.
-  if (kLora ? warp >= 2 && warp <= 5 : warp != 0) {  // (the weight producer: once its first ring of weights is on its way)
+  // (The producers wait for themselves: that of the weights once its first ring is on its way.)
+  if (kLora ? warp >= 2 && warp <= 5 : warp != 0) {
     grid_dependency_wait();
     allow_dependent_launch();
   }
 
-  // The sequences of a unit that take further k-steps for their adapters: calls
+  // The sequences of a unit that take further k-steps for their adapters (whole warp): calls
   // step(sequence of the tile, adapter, rank chunk of 64) in order until it returns false.
   auto adapter_steps = [&](const PItem& it, const PUnit& u, auto&& step) -> bool {
     if constexpr (kLora) {
       if (u.p != 0 || it.k1 != a.k_steps) return true;
       const PProblem& P = a.pr[0];
-      const int seq0 = u.mt * P.seq_per_unit, n = min(P.seq_per_unit, a.b - seq0);
-      for (int i = 0; i < n; ++i) {
-        const int ad = lora.bank.adapter_of[seq0 + i];
-        if (ad < 0 || ad >= lora.bank.n_adapters) continue;
+      const int seq0 = u.mt * P.seq_per_unit, n = min(P.seq_per_unit, a.b - seq0);  // at most 16
+      const int mine = lane < n ? lora.bank.adapter_of[seq0 + lane] : -1;
+      for (unsigned todo = __ballot_sync(0xffffffffu, mine >= 0 && mine < lora.bank.n_adapters); todo; todo &= todo - 1) {
+        const int i = __ffs(int(todo)) - 1, ad = __shfl_sync(0xffffffffu, mine, i);
         for (int rc = 0; rc < lora.bank.rank; rc += kPKStep)
           if (!step(i, ad, rc)) return false;
       }
@@ -246,111 +256,136 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
     return true;
   };
 
-  if (warp == 0 || warp == 6) {
-    // ------------------------------------------------------------ TMA producers
-    // warp 0: the weights (A) of every k-step; warp 6: the activations (B)
-    bool waited = !kLora && warp != 0;
-    if (lane == 0) {
-      const bool is_a = warp == 0;
-      const int nst = is_a ? kPAStages : kPBStages;
-      prefetch_map(is_a ? &w0 : &x0);
-      prefetch_map(is_a ? &w1 : &x1);
-      const uint64_t pol = is_a ? l2_evict_first() : l2_evict_last();
-      bool ok = true;
-      int k = 0;
-      for (int i = 0; i < w.n_items && ok; ++i) {
-        const PItem it = item_of(a, w, i);
-        const PUnit u = unit_of(a, it.u);
-        const PProblem& P = a.pr[u.p];
-        const CUtensorMap* m = is_a ? (u.p ? &w1 : &w0) : (u.p ? &x1 : &x0);
-        const uint32_t bytes = is_a ? uint32_t(kPABytes) : uint32_t(P.load_rows * kPKStep * 2);
-        // the weights are read once: they must not push the activations (read again by
-        // every weight tile of the layer) out of L2
-        // k-step k's stage of this ring is free for its next copy (false: gave up)
-        auto begin_step = [&](uint32_t n_bytes) -> bool {
-          if (!kLora && k == nst && !waited) {  // (the first ring's weights are in flight)
-            grid_dependency_wait();
-            allow_dependent_launch();
-            waited = true;
-          }
-          // the stage is free once the MMAs of the k-step that used it before have completed
-          // (k - nst); the MMAs of a k-step complete in order, and the one wait before for
-          // the same barrier covered its previous phase, so the parity names this phase
-          const int prev = k - nst;
-          if (prev >= 0 && !pwait(s, &s.aempty[prev % kPAStages], uint32_t(prev / kPAStages) & 1, a.err)) return false;
-          mbar_arrive_expect_tx(&s.afull[k % kPAStages], n_bytes);
-          return true;
-        };
-        for (int ks = it.k0; ks < it.k1; ++ks, ++k) {
-          const int st = k % nst;                    // this ring's stage
-          uint64_t* full = &s.afull[k % kPAStages];  // the k-step's barrier
-          if (!begin_step(bytes)) { ok = false; break; }
-          if (is_a)
-            tma_load_2d_hint(a_ring + st * kPABytes, m, ks * kPKStep, u.l * P.n_out + u.nt * kPTileN, full, pol);
-          else if (P.is_4d)
-            tma_load_4d_hint(b_ring + st * kPBBytes, m, ks * kPKStep, 0, u.l, u.mt * P.seq_per_unit, full, pol);
-          else
-            tma_load_3d_hint(b_ring + st * kPBBytes, m, ks * kPKStep, u.l, u.mt * P.seq_per_unit, full, pol);
-        }
-        if (!ok) break;
-        ok = adapter_steps(it, u, [&](int i, int ad, int rc) -> bool {
-          const int st = k % nst;
-          uint64_t* full = &s.afull[k % kPAStages];
-          if (!waited) {
-            grid_dependency_wait();
-            allow_dependent_launch();
-            waited = true;
-          }
-          if (!begin_step(is_a ? uint32_t(kPABytes) : uint32_t(2 * P.pitch * kPKStep * 2))) return false;
-          if (is_a)
-            tma_load_2d(a_ring + st * kPABytes, &wl, rc, (ad * a.L + u.l) * P.n_out + u.nt * kPTileN, full);
-          else
-            tma_load_2d(b_ring + st * kPBBytes, &xl, rc,
-                        ((u.mt * P.seq_per_unit + i) * a.L + u.l) * 2 * P.pitch, full);
-          ++k;
-          return true;
-        });
-      }
-      s.issued[is_a ? 0 : 1] = k;
-    }
-    if (!waited) {  // (every thread of the CTA passes the wait before it triggers)
+  // (The producers and the MMA issuer walk their loops as whole warps, one elected lane issuing:
+  // what the loops work out is then the same in every lane, as the issued instructions want it.)
+  auto produce = [&](auto weights) {
+    constexpr bool is_a = decltype(weights)::value;
+    constexpr int nst = is_a ? kPAStages : kPBStages;
+    unsigned char* const ring = is_a ? a_ring : b_ring;
+    constexpr int kBytes = is_a ? kPABytes : kPBBytes;
+    // the weights are read once: they must not push the activations (read again by
+    // every weight tile of the layer) out of L2
+    const uint64_t pol = is_a ? l2_evict_first() : l2_evict_last();
+    bool waited = !kLora && !is_a, ok = true;
+    auto wait_grid = [&]() {
+      if (waited) return;
       grid_dependency_wait();
       allow_dependent_launch();
+      waited = true;
+    };
+    int k = 0, st = 0, bar = 0;      // k-step; its stage of this ring; its barrier
+    int back = 0, back_parity = 0;   // k - nst's barrier and its phase
+    // k-step k's stage is free for its next copy (false: gave up): the MMAs of the k-step that
+    // used it before (k - nst) have completed. The MMAs of a k-step complete in order, and the
+    // one wait before for the same barrier covered its previous phase, so the parity names this
+    // phase.
+    auto begin_step = [&]() -> bool {
+      if (k < nst) return true;
+      if (!kLora) wait_grid();  // (the first ring's weights are in flight)
+      if (!pwait_warp(s, &s.aempty[back], uint32_t(back_parity), a.err)) return false;
+      if (++back == kPAStages) { back = 0; back_parity ^= 1; }
+      return true;
+    };
+    auto end_step = [&]() {
+      __syncwarp();
+      ++k;
+      if (++st == nst) st = 0;
+      if (++bar == kPAStages) bar = 0;
+    };
+    for (int i = 0; i < w.n_items && ok; ++i) {
+      const PItem it = item_of(a, w, i);
+      const PUnit u = unit_of(a, it.u);
+      const PProblem& P = a.pr[u.p];
+      const CUtensorMap* m = is_a ? (u.p ? &w1 : &w0) : (u.p ? &x1 : &x0);
+      const uint32_t bytes = is_a ? uint32_t(kPABytes) : uint32_t(P.load_rows * kPKStep * 2);
+      const int row = is_a ? u.l * P.n_out + u.nt * kPTileN : u.mt * P.seq_per_unit;
+      const bool is_4d = P.is_4d;
+      for (int ks = it.k0; ks < it.k1; ++ks) {
+        if (!begin_step()) { ok = false; break; }
+        if (elect_one()) {
+          uint64_t* full = &s.afull[bar];
+          mbar_arrive_expect_tx(full, bytes);
+          if constexpr (is_a) tma_load_2d_hint(ring + st * kBytes, m, ks * kPKStep, row, full, pol);
+          else if (is_4d) tma_load_4d_hint(ring + st * kBytes, m, ks * kPKStep, 0, u.l, row, full, pol);
+          else tma_load_3d_hint(ring + st * kBytes, m, ks * kPKStep, u.l, row, full, pol);
+        }
+        end_step();
+      }
+      if (!ok) break;
+      ok = adapter_steps(it, u, [&](int i, int ad, int rc) -> bool {
+        wait_grid();
+        if (!begin_step()) return false;
+        if (elect_one()) {
+          uint64_t* full = &s.afull[bar];
+          mbar_arrive_expect_tx(full, is_a ? uint32_t(kPABytes) : uint32_t(2 * P.pitch * kPKStep * 2));
+          if constexpr (is_a)
+            tma_load_2d(ring + st * kBytes, &wl, rc, (ad * a.L + u.l) * P.n_out + u.nt * kPTileN, full);
+          else
+            tma_load_2d(ring + st * kBytes, &xl, rc, ((row + i) * a.L + u.l) * 2 * P.pitch, full);
+        }
+        end_step();
+        return true;
+      });
     }
+    if (lane == 0) s.issued[is_a ? 0 : 1] = k;
+    wait_grid();  // (every thread of the CTA passes the wait before it triggers)
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producers
+    // warp 0: the weights (A) of every k-step; warp 6: the activations (B)
+    if (lane == 0) { prefetch_map(&w0); prefetch_map(&w1); }
+    produce(std::true_type{});
+  } else if (warp == 6) {
+    if (lane == 0) { prefetch_map(&x0); prefetch_map(&x1); }
+    produce(std::false_type{});
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      bool ok = true;
-      int k = 0;
-      for (int i = 0; i < w.n_items && ok; ++i) {
-        const PItem it = item_of(a, w, i);
-        const PUnit u = unit_of(a, it.u);
-        const PProblem& P = a.pr[u.p];
-        const int ab = i & 1;
-        if (!pwait(s, &s.acc_empty[ab], ((i >> 1) & 1) ^ 1, a.err)) break;
-        tc_fence_after();
-        const uint32_t id = idesc_bf16(P.act_rows, false, kPTileN);
-        const uint32_t d = tmem + uint32_t(ab * kPMaxAct);
-        for (int ks = it.k0; ks < it.k1; ++ks, ++k) {
-          const int sa = k % kPAStages, sb = k % kPBStages;
-          if (!pwait(s, &s.afull[sa], (k / kPAStages) & 1, a.err)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t da = sdesc(smem_u32(a_ring + sa * kPABytes), 16, 1024);
-          const uint64_t db = sdesc(smem_u32(b_ring + sb * kPBBytes), 16, 1024);
+    bool ok = true;
+    int sa = 0, sb = 0;       // the k-step's stages
+    uint32_t parity = 0;      // of its barrier
+    const uint64_t da0 = sdesc(smem_u32(a_ring), 16, 1024), db0 = sdesc(smem_u32(b_ring), 16, 1024);
+    bool ready = false;       // the k-step's copies were seen complete during the one before
+    auto begin_step = [&]() -> bool {
+      if (!__all_sync(0xffffffffu, ready) && !pwait_warp(s, &s.afull[sa], parity, a.err)) return false;
+      tc_fence_after();
+      // asked now, needed after the MMAs' issue (an answer takes about 200 cycles)
+      const bool wrap = sa + 1 == kPAStages;
+      ready = mbar_test(&s.afull[wrap ? 0 : sa + 1], parity ^ uint32_t(wrap));
+      return true;
+    };
+    auto end_step = [&]() {
+      __syncwarp();
+      if (++sa == kPAStages) { sa = 0; parity ^= 1; }
+      if (++sb == kPBStages) sb = 0;
+    };
+    for (int i = 0; i < w.n_items && ok; ++i) {
+      const PItem it = item_of(a, w, i);
+      const PUnit u = unit_of(a, it.u);
+      const PProblem& P = a.pr[u.p];
+      const int ab = i & 1;
+      if (!pwait_warp(s, &s.acc_empty[ab], ((i >> 1) & 1) ^ 1, a.err)) break;
+      tc_fence_after();
+      const uint32_t id = idesc_bf16(P.act_rows, false, kPTileN);
+      const uint32_t d = tmem + uint32_t(ab * kPMaxAct);
+      for (int ks = it.k0; ks < it.k1; ++ks) {
+        if (!begin_step()) { ok = false; break; }
+        const uint64_t da = da0 + uint32_t(sa * (kPABytes >> 4)), db = db0 + uint32_t(sb * (kPBBytes >> 4));
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kPKStep / 16; ++kk)  // K = 16 per MMA: 32 bytes along the row
             mma_bf16(d, da + uint32_t(kk * 2), db + uint32_t(kk * 2), id, (ks > it.k0 || kk > 0) ? 1u : 0u);
           mma_commit(&s.aempty[sa]);  // frees both stages of the k-step
         }
-        if (ok)
-          ok = adapter_steps(it, u, [&](int i, int, int rc) -> bool {
-            const int sa = k % kPAStages, sb = k % kPBStages;
-            if (!pwait(s, &s.afull[sa], (k / kPAStages) & 1, a.err)) return false;
-            tc_fence_after();
-            const uint64_t da = sdesc(smem_u32(a_ring + sa * kPABytes), 16, 1024);
-            const uint64_t db = sdesc(smem_u32(b_ring + sb * kPBBytes), 16, 1024);
-            const uint32_t ids = idesc_bf16(P.pitch, false, kPTileN), ds = d + uint32_t(i * P.pitch);
-            const uint32_t low_part = uint32_t(P.pitch * kPKStep * 2 >> 4);
+        end_step();
+      }
+      if (ok)
+        ok = adapter_steps(it, u, [&](int i, int, int rc) -> bool {
+          if (!begin_step()) return false;
+          const uint64_t da = da0 + uint32_t(sa * (kPABytes >> 4)), db = db0 + uint32_t(sb * (kPBBytes >> 4));
+          const uint32_t ids = idesc_bf16(P.pitch, false, kPTileN), ds = d + uint32_t(i * P.pitch);
+          const uint32_t low_part = uint32_t(P.pitch * kPKStep * 2 >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kPKStep / 16; ++kk) {
               if (rc + 16 * kk >= lora.bank.rank) break;
@@ -359,14 +394,14 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
                 mma_bf16(ds, da + uint32_t(kk * 2), db + part * low_part + uint32_t(kk * 2), ids, 1u);
             }
             mma_commit(&s.aempty[sa]);
-            ++k;
-            return true;
-          });
-        if (ok) mma_commit(&s.acc_full[ab]);
-      }
+          }
+          end_step();
+          return true;
+        });
+      if (ok && elect_one()) mma_commit(&s.acc_full[ab]);
+      __syncwarp();
     }
     if (kLora) {  // (every thread passes the wait before it triggers)
-      __syncwarp();
       grid_dependency_wait();
       allow_dependent_launch();
     }
@@ -498,9 +533,9 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
       if (n > 0) mbar_wait_bounded(&s.afull[st], uint32_t(n - 1) & 1, kWaitLimit);
     }
   }
-  if (warp == 1 && lane == 0 && s.abort) {
+  if (warp == 1 && s.abort && elect_one()) {
     // and the MMAs issued so far, before TMEM is released
-    mma_commit(&s.drain);  // tracks every MMA this thread issued
+    mma_commit(&s.drain);  // tracks every MMA this thread (the same one each time) issued
     mbar_wait_bounded(&s.drain, 0, kWaitLimit);
   }
   tc_fence_before();
@@ -543,7 +578,8 @@ __global__ void __launch_bounds__(low_warps(NT) * 32) lora_low_kernel(const __gr
   __shared__ float low_s[kLoraMaxRank];
   const int R = lora.bank.rank;
   const int b = int(blockIdx.x) / L, l = int(blockIdx.x) - b * L;
-  const int p = blockIdx.y + 1 == gridDim.y;  // the last CTA of a (sequence, layer): its boundary row, the whole rank
+  // the first CTAs, which have most to do: a (sequence, layer)'s boundary row, the whole rank
+  const int p = blockIdx.y == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rows = p ? 1 : B;
   grid_dependency_wait();
@@ -563,7 +599,7 @@ __global__ void __launch_bounds__(low_warps(NT) * 32) lora_low_kernel(const __gr
   const float scale = lora.bank.scale[ad];
   const int pitch = (B + 15) & ~15;  // (rows past the block feed columns that are not stored)
   __nv_bfloat16* split = lora.split + (int64_t(b) * L + l) * 2 * pitch * R;
-  for (int r0 = p ? 0 : int(blockIdx.y) * 8 * NT; r0 < R; r0 += 8 * NT) {
+  for (int r0 = p ? 0 : int(blockIdx.y - 1) * 8 * NT; r0 < R; r0 += 8 * NT) {
     const int nr = min(8 * NT, R - r0);
     const __nv_bfloat16* wr[NT];
 #pragma unroll

@@ -100,6 +100,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn_major, int m 
          | (uint32_t(n >> 3) << 17)
          | (uint32_t(m >> 4) << 24);
 }
+// One lane of the (converged) warp, the same one each time.
+__device__ inline bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ inline void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
