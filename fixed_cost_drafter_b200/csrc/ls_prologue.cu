@@ -566,11 +566,47 @@ __device__ inline void mma_bf16_warp(float (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// This warp's part of acc = x A^T: 32 of every 32 W hidden entries. xr: the rows g and g + 8 of
+// MT 16-row tiles (or, with one row, that row); wr: row g of NT 8-row tiles of A; both from this
+// thread's entry on.
+template <int MT, int NT, int W, int NX>
+__device__ inline void low_products(float (&acc)[MT][NT][4], const __nv_bfloat16* const (&xr)[NX],
+                                    const __nv_bfloat16* const (&wr)[NT], int hidden, int warp) {
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+  constexpr int kAhead = NX + NT <= 4 ? 4 : (NX + NT <= 6 ? 3 : 2);  // steps whose loads are in flight together
+  for (int k0 = warp * 32; k0 < hidden; k0 += 32 * W * kAhead) {
+    uint4 av[kAhead][NX], bv[kAhead][NT];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const int k = min(k0 + 32 * W * s, hidden - 32);
+#pragma unroll
+      for (int m = 0; m < NX; ++m) av[s][m] = ld_nc_v4(xr[m] + k);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) bv[s][n] = ld_nc_v4(wr[n] + k);
+    }
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      if (k0 + 32 * W * s >= hidden) break;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint4 &lo = av[s][NX == 1 ? 0 : 2 * m], &hi = av[s][NX == 1 ? 0 : 2 * m + 1];
+          mma_bf16_warp(acc[m][n], lo.x, hi.x, lo.y, hi.y, bv[s][n].x, bv[s][n].y);
+          mma_bf16_warp(acc[m][n], lo.z, hi.z, lo.w, hi.w, bv[s][n].z, bv[s][n].w);
+        }
+    }
+  }
+}
+
 // MT: 16-row tiles of activation rows (block rows up to 32). NT: 8-entry tiles of the rank. (Rows
 // and rank entries past the last are read as the last one again and not stored: with a branch
 // per tile the loads would wait for one another.)
 template <int MT, int NT>
-__global__ void __launch_bounds__(low_warps(NT) * 32) lora_low_kernel(const __grid_constant__ PLora lora, const __nv_bfloat16* x,
+__global__ void __launch_bounds__(low_warps(NT) * 32, NT == 4 ? 2 : 1) lora_low_kernel(const __grid_constant__ PLora lora, const __nv_bfloat16* x,
                                                                   const __nv_bfloat16* boundary, int L, int B,
                                                                   int hidden, int n_kv, int32_t* err) {
   constexpr int kLowWarps = low_warps(NT);
@@ -579,9 +615,8 @@ __global__ void __launch_bounds__(low_warps(NT) * 32) lora_low_kernel(const __gr
   const int R = lora.bank.rank;
   const int b = int(blockIdx.x) / L, l = int(blockIdx.x) - b * L;
   // the first CTAs, which have most to do: a (sequence, layer)'s boundary row, the whole rank
-  const int p = blockIdx.y == 0;
+  const bool p = blockIdx.y == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rows = p ? 1 : B;
   grid_dependency_wait();
   allow_dependent_launch();
   const int ad = lora.bank.adapter_of[b];
@@ -589,49 +624,21 @@ __global__ void __launch_bounds__(low_warps(NT) * 32) lora_low_kernel(const __gr
     if (ad != -1 && threadIdx.x == 0) set_err(err, LS_DEVERR_ADAPTER);
     return;
   }
-  const __nv_bfloat16* src = (p ? boundary : x) + (int64_t(b) * L + l) * rows * hidden + t * 8;
   const __nv_bfloat16* bank = static_cast<const __nv_bfloat16*>(p ? lora.bank.a_kv : lora.bank.a_q) +
                               (int64_t(ad) * L + l) * R * hidden + t * 8;
-  // (rows past the last are read as the last one again and not stored)
-  const __nv_bfloat16* xr[2 * MT];
-#pragma unroll
-  for (int m = 0; m < 2 * MT; ++m) xr[m] = src + int64_t(min(m * 8 + g, rows - 1)) * hidden;
   const float scale = lora.bank.scale[ad];
-  const int pitch = (B + 15) & ~15;  // (rows past the block feed columns that are not stored)
-  __nv_bfloat16* split = lora.split + (int64_t(b) * L + l) * 2 * pitch * R;
-  for (int r0 = p ? 0 : int(blockIdx.y - 1) * 8 * NT; r0 < R; r0 += 8 * NT) {
-    const int nr = min(8 * NT, R - r0);
-    const __nv_bfloat16* wr[NT];
+  if (!p) {
+    const int r0 = int(blockIdx.y - 1) * 8 * NT, nr = min(8 * NT, R - r0);
+    const __nv_bfloat16 *xr[2 * MT], *wr[NT];
+#pragma unroll
+    for (int m = 0; m < 2 * MT; ++m)
+      xr[m] = x + ((int64_t(b) * L + l) * B + min(m * 8 + g, B - 1)) * hidden + t * 8;
 #pragma unroll
     for (int n = 0; n < NT; ++n) wr[n] = bank + int64_t(r0 + min(8 * n + g, nr - 1)) * hidden;
     float acc[MT][NT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-    constexpr int kAhead = 2 * MT + NT <= 4 ? 4 : 2;  // steps whose loads are in flight together
-    for (int k0 = warp * 32; k0 < hidden; k0 += 32 * kLowWarps * kAhead) {
-      uint4 av[kAhead][2 * MT], bv[kAhead][NT];
-#pragma unroll
-      for (int s = 0; s < kAhead; ++s) {
-        const int k = min(k0 + 32 * kLowWarps * s, hidden - 32);
-#pragma unroll
-        for (int m = 0; m < 2 * MT; ++m) av[s][m] = ld_nc_v4(xr[m] + k);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) bv[s][n] = ld_nc_v4(wr[n] + k);
-      }
-#pragma unroll
-      for (int s = 0; s < kAhead; ++s) {
-        if (k0 + 32 * kLowWarps * s >= hidden) break;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            mma_bf16_warp(acc[m][n], av[s][2 * m].x, av[s][2 * m + 1].x, av[s][2 * m].y, av[s][2 * m + 1].y, bv[s][n].x, bv[s][n].y);
-            mma_bf16_warp(acc[m][n], av[s][2 * m].z, av[s][2 * m + 1].z, av[s][2 * m].w, av[s][2 * m + 1].w, bv[s][n].z, bv[s][n].w);
-          }
-      }
-    }
+    low_products<MT, NT, kLowWarps>(acc, xr, wr, hidden, warp);
+    const int pitch = (B + 15) & ~15;  // (rows past the block feed columns that are not stored)
+    __nv_bfloat16* split = lora.split + (int64_t(b) * L + l) * 2 * pitch * R;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -642,36 +649,65 @@ __global__ void __launch_bounds__(low_warps(NT) * 32) lora_low_kernel(const __gr
       __syncthreads();
       for (int i = threadIdx.x; i < 16 * nr; i += kLowWarps * 32) {
         const int row = 16 * m + i / nr, r = i % nr;
-        if (row >= rows) break;
+        if (row >= B) break;
         float sum = 0.f;
 #pragma unroll
         for (int v = 0; v < kLowWarps; ++v) sum += red[v][i / nr][r];
         sum *= scale;
-        if (p) {
-          low_s[r0 + r] = sum;
-        } else {
-          const __nv_bfloat16 hi = __float2bfloat16_rn(sum);
-          const float rest = sum - __bfloat162float(hi);
-          split[row * R + r0 + r] = hi;
-          split[(pitch + row) * R + r0 + r] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.f);  // (an infinite sum stays infinite)
-        }
+        const __nv_bfloat16 hi = __float2bfloat16_rn(sum);
+        const float rest = sum - __bfloat162float(hi);
+        split[row * R + r0 + r] = hi;
+        split[(pitch + row) * R + r0 + r] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.f);  // (an infinite sum stays infinite)
       }
       __syncthreads();
     }
-    if (!p) return;
+    return;
   }
-  // the boundary row's outputs, a weight row per thread
-  const __nv_bfloat16* wb = static_cast<const __nv_bfloat16*>(lora.bank.b_kv) + (int64_t(ad) * L + l) * n_kv * R;
-  for (int n = threadIdx.x; n < n_kv; n += kLowWarps * 32) {
-    float y = 0.f;
-#pragma unroll 4
-    for (int e = 0; e < R; e += 8) {
-      float f[8];
-      Elem<__nv_bfloat16>::to_f32(ld_nc_v4(wb + int64_t(n) * R + e), f);
+  const __nv_bfloat16* const xr[1] = {boundary + (int64_t(b) * L + l) * hidden + t * 8};
+  float* const part = &red[0][0][0];  // [warps][8 NT]
+  for (int r0 = 0; r0 < R; r0 += 8 * NT) {
+    const int nr = min(8 * NT, R - r0);
+    const __nv_bfloat16* wr[NT];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) y = fmaf(f[q], low_s[e + q], y);
+    for (int n = 0; n < NT; ++n) wr[n] = bank + int64_t(r0 + min(8 * n + g, nr - 1)) * hidden;
+    float acc[1][NT][4];
+    low_products<1, NT, kLowWarps>(acc, xr, wr, hidden, warp);
+    if (g == 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(part + (warp * NT + n) * 8 + 2 * t) = make_float2(acc[0][n][0], acc[0][n][1]);
     }
-    lora.add[(int64_t(b) * L + l) * n_kv + n] = y;
+    __syncthreads();
+    if (int(threadIdx.x) < nr) {
+      float sum = 0.f;
+#pragma unroll
+      for (int v = 0; v < kLowWarps; ++v) sum += part[v * NT * 8 + threadIdx.x];
+      low_s[r0 + threadIdx.x] = sum * scale;
+    }
+    __syncthreads();
+  }
+  // the boundary row's outputs: kOut weight rows per thread at a time, their loads together
+  constexpr int kOut = 4, kThreads = kLowWarps * 32;
+  const __nv_bfloat16* wb = static_cast<const __nv_bfloat16*>(lora.bank.b_kv) + (int64_t(ad) * L + l) * n_kv * R;
+  float* add = lora.add + (int64_t(b) * L + l) * n_kv;
+  for (int n0 = threadIdx.x; n0 < n_kv; n0 += kOut * kThreads) {
+    float y[kOut] = {};
+#pragma unroll 2
+    for (int e = 0; e < R; e += 8) {
+      uint4 w[kOut];
+#pragma unroll
+      for (int u = 0; u < kOut; ++u) w[u] = ld_nc_v4(wb + int64_t(min(n0 + u * kThreads, n_kv - 1)) * R + e);
+#pragma unroll
+      for (int u = 0; u < kOut; ++u) {
+        float f[8];
+        Elem<__nv_bfloat16>::to_f32(w[u], f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) y[u] = fmaf(f[q], low_s[e + q], y[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kOut; ++u)
+      if (n0 + u * kThreads < n_kv) add[n0 + u * kThreads] = y[u];
   }
 }
 
