@@ -549,11 +549,15 @@ prologue_kernel(const __grid_constant__ PArgs a, const __grid_constant__ PLora l
 // low = scale (A x), a CTA per (sequence, layer) and 8 NT of the rank, and one for its boundary row
 // (the whole rank, and its outputs).
 // Its bytes (x and A once each) are few beside the weights'; what counts is the latency, as the
-// projections' kernel follows: 16 warps spread over the hidden size, 32 entries at a time (a
-// thread's 16-byte load of eight entries of a row is its part of two m16n8k16 products' operands,
-// their k order is free), with the loads of several steps in flight at once. The warps' sums are
-// added in warp order. (Run beside the projections instead, a warp per 8 of the rank and no shared
-// memory, it took longer than their first units: 160 us instead of 82 for 16 requests at rank 16.)
+// projections' kernel follows: the warps spread over the hidden size, 64 entries at a time. A
+// thread's 32-byte load of sixteen entries of a row is its part of four m16n8k16 products'
+// operands (their k order is free), and a row's four threads read a whole 128-byte line: with
+// 16-byte loads, half lines, the L1 cache was the bound (64 requests at rank 64: 57 us instead of
+// 47, 16 at rank 16: 13 instead of 9). Where x or A is not 32-byte aligned, two 16-byte loads take
+// its place. The warps' sums are added in warp order. Boundary rows grouped by adapter, so that A
+// and B are read once for several of them, made their CTAs' chains longer: 60 us. (Run beside the
+// projections instead, a warp per 8 of the rank and no shared memory, it took longer than their
+// first units: 160 us instead of 82 for 16 requests at rank 16.)
 // (two CTAs per SM with 8 warps where the loads in flight need the registers)
 __host__ __device__ constexpr int low_warps(int nt) { return nt <= 2 ? 16 : 8; }
 constexpr int kLoraMaxRank = 128;
@@ -566,38 +570,49 @@ __device__ inline void mma_bf16_warp(float (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// This warp's part of acc = x A^T: 32 of every 32 W hidden entries. xr: the rows g and g + 8 of
+// This warp's part of acc = x A^T: 64 of every 64 W hidden entries. xr: the rows g and g + 8 of
 // MT 16-row tiles (or, with one row, that row); wr: row g of NT 8-row tiles of A; both from this
 // thread's entry on.
-template <int MT, int NT, int W, int NX>
+template <int MT, int NT, int W, bool kWide, int NX>
 __device__ inline void low_products(float (&acc)[MT][NT][4], const __nv_bfloat16* const (&xr)[NX],
                                     const __nv_bfloat16* const (&wr)[NT], int hidden, int warp) {
+  auto load = [](const __nv_bfloat16* p, uint4 (&v)[2]) {
+    if constexpr (kWide) {
+      ld_nc_v8(p, v[0], v[1]);
+    } else {
+      v[0] = ld_nc_v4(p);
+      v[1] = ld_nc_v4(p + 8);
+    }
+  };
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-  constexpr int kAhead = NX + NT <= 4 ? 4 : (NX + NT <= 6 ? 3 : 2);  // steps whose loads are in flight together
-  for (int k0 = warp * 32; k0 < hidden; k0 += 32 * W * kAhead) {
-    uint4 av[kAhead][NX], bv[kAhead][NT];
+  constexpr int kAhead = NX + NT <= 4 ? 2 : 1;  // steps whose loads are in flight together
+#pragma unroll 1
+  for (int k0 = warp * 64; k0 < hidden; k0 += 64 * W * kAhead) {
+    uint4 av[kAhead][NX][2], bv[kAhead][NT][2];
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
-      const int k = min(k0 + 32 * W * s, hidden - 32);
+      const int k = min(k0 + 64 * W * s, hidden - 64);
 #pragma unroll
-      for (int m = 0; m < NX; ++m) av[s][m] = ld_nc_v4(xr[m] + k);
+      for (int m = 0; m < NX; ++m) load(xr[m] + k, av[s][m]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) bv[s][n] = ld_nc_v4(wr[n] + k);
+      for (int n = 0; n < NT; ++n) load(wr[n] + k, bv[s][n]);
     }
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
-      if (k0 + 32 * W * s >= hidden) break;
+      if (k0 + 64 * W * s >= hidden) break;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint4 &lo = av[s][NX == 1 ? 0 : 2 * m], &hi = av[s][NX == 1 ? 0 : 2 * m + 1];
-          mma_bf16_warp(acc[m][n], lo.x, hi.x, lo.y, hi.y, bv[s][n].x, bv[s][n].y);
-          mma_bf16_warp(acc[m][n], lo.z, hi.z, lo.w, hi.w, bv[s][n].z, bv[s][n].w);
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint4 &lo = av[s][NX == 1 ? 0 : 2 * m][h], &hi = av[s][NX == 1 ? 0 : 2 * m + 1][h], &w = bv[s][n][h];
+            mma_bf16_warp(acc[m][n], lo.x, hi.x, lo.y, hi.y, w.x, w.y);
+            mma_bf16_warp(acc[m][n], lo.z, hi.z, lo.w, hi.w, w.z, w.w);
+          }
     }
   }
 }
@@ -605,7 +620,7 @@ __device__ inline void low_products(float (&acc)[MT][NT][4], const __nv_bfloat16
 // MT: 16-row tiles of activation rows (block rows up to 32). NT: 8-entry tiles of the rank. (Rows
 // and rank entries past the last are read as the last one again and not stored: with a branch
 // per tile the loads would wait for one another.)
-template <int MT, int NT>
+template <int MT, int NT, bool kWide>
 __global__ void __launch_bounds__(low_warps(NT) * 32, NT == 4 ? 2 : 1) lora_low_kernel(const __grid_constant__ PLora lora, const __nv_bfloat16* x,
                                                                   const __nv_bfloat16* boundary, int L, int B,
                                                                   int hidden, int n_kv, int32_t* err) {
@@ -625,18 +640,18 @@ __global__ void __launch_bounds__(low_warps(NT) * 32, NT == 4 ? 2 : 1) lora_low_
     return;
   }
   const __nv_bfloat16* bank = static_cast<const __nv_bfloat16*>(p ? lora.bank.a_kv : lora.bank.a_q) +
-                              (int64_t(ad) * L + l) * R * hidden + t * 8;
+                              (int64_t(ad) * L + l) * R * hidden + t * 16;
   const float scale = lora.bank.scale[ad];
   if (!p) {
     const int r0 = int(blockIdx.y - 1) * 8 * NT, nr = min(8 * NT, R - r0);
     const __nv_bfloat16 *xr[2 * MT], *wr[NT];
 #pragma unroll
     for (int m = 0; m < 2 * MT; ++m)
-      xr[m] = x + ((int64_t(b) * L + l) * B + min(m * 8 + g, B - 1)) * hidden + t * 8;
+      xr[m] = x + ((int64_t(b) * L + l) * B + min(m * 8 + g, B - 1)) * hidden + t * 16;
 #pragma unroll
     for (int n = 0; n < NT; ++n) wr[n] = bank + int64_t(r0 + min(8 * n + g, nr - 1)) * hidden;
     float acc[MT][NT][4];
-    low_products<MT, NT, kLowWarps>(acc, xr, wr, hidden, warp);
+    low_products<MT, NT, kLowWarps, kWide>(acc, xr, wr, hidden, warp);
     const int pitch = (B + 15) & ~15;  // (rows past the block feed columns that are not stored)
     __nv_bfloat16* split = lora.split + (int64_t(b) * L + l) * 2 * pitch * R;
 #pragma unroll
@@ -663,7 +678,7 @@ __global__ void __launch_bounds__(low_warps(NT) * 32, NT == 4 ? 2 : 1) lora_low_
     }
     return;
   }
-  const __nv_bfloat16* const xr[1] = {boundary + (int64_t(b) * L + l) * hidden + t * 8};
+  const __nv_bfloat16* const xr[1] = {boundary + (int64_t(b) * L + l) * hidden + t * 16};
   float* const part = &red[0][0][0];  // [warps][8 NT]
   for (int r0 = 0; r0 < R; r0 += 8 * NT) {
     const int nr = min(8 * NT, R - r0);
@@ -671,7 +686,7 @@ __global__ void __launch_bounds__(low_warps(NT) * 32, NT == 4 ? 2 : 1) lora_low_
 #pragma unroll
     for (int n = 0; n < NT; ++n) wr[n] = bank + int64_t(r0 + min(8 * n + g, nr - 1)) * hidden;
     float acc[1][NT][4];
-    low_products<1, NT, kLowWarps>(acc, xr, wr, hidden, warp);
+    low_products<1, NT, kLowWarps, kWide>(acc, xr, wr, hidden, warp);
     if (g == 0) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -820,9 +835,15 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
     lc.attrs = la;
     lc.numAttrs = 1;
     const bool two = p.B > 16;
-    const auto low_kernel = tiles == 1   ? (two ? lora_low_kernel<2, 1> : lora_low_kernel<1, 1>)
-                            : tiles == 2 ? (two ? lora_low_kernel<2, 2> : lora_low_kernel<1, 2>)
-                                         : (two ? lora_low_kernel<2, 4> : lora_low_kernel<1, 4>);
+    const bool wide = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(lora->a_q) |
+                        reinterpret_cast<uintptr_t>(lora->a_kv)) & 31) == 0;  // (rows are whole 128 bytes, the boundary view is aligned)
+    auto pick = [&](auto w) {
+      constexpr bool kWide = decltype(w)::value;
+      return tiles == 1   ? (two ? lora_low_kernel<2, 1, kWide> : lora_low_kernel<1, 1, kWide>)
+             : tiles == 2 ? (two ? lora_low_kernel<2, 2, kWide> : lora_low_kernel<1, 2, kWide>)
+                          : (two ? lora_low_kernel<2, 4, kWide> : lora_low_kernel<1, 4, kWide>);
+    };
+    const auto low_kernel = wide ? pick(std::true_type{}) : pick(std::false_type{});
     e = cudaLaunchKernelEx(&lc, low_kernel, pl,
                            static_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(p.boundary),
                            p.L, p.B, p.hidden, K.n_out, p.err);

@@ -98,6 +98,30 @@ def test_large_projection():
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("rank,block", [(8, 16), (16, 5), (64, 16), (24, 32)])
+def test_arguments_on_16_byte_boundaries(rank, block):
+    """The documented alignment is 16 bytes: the same bits as from more aligned arguments."""
+    c = Case(5, block, 2, 320, rank, 3, [2, 0, -1, 2, 1], q_heads=4, seed=11)
+    want = c.run()
+    c.check(*want)
+
+    def moved(t):
+        m = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")[8:].view(t.shape).copy_(t)
+        assert m.data_ptr() % 32 == 16
+        return m
+
+    for names in (("x",), ("a_q",), ("a_kv",), ("x", "a_q", "b_q", "a_kv", "b_kv", "w_q", "w_kv")):
+        kept = {n: getattr(c, n) for n in names}
+        for n, t in kept.items():
+            setattr(c, n, moved(t))
+        c.desc = F.make_lora(c.na, c.r, c.a_q, c.b_q, c.a_kv, c.b_kv, c.scale, c.which)
+        got = c.run()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        for n, t in kept.items():
+            setattr(c, n, t)
+    assert c.lib.error() == (F.LS_OK, 0)
+
+
 def test_adapters_do_not_reach_other_sequences():
     """An adapter with infinities and NaN changes its own sequences only."""
     which = [0, 1, -1, 2, 1, 0, 2]
