@@ -20,6 +20,8 @@
 // epilogue (one TMEM subpartition each: a thread owns one weight row, its outputs go
 // through a shared-memory tile so that whole 256-byte output rows leave as 16-byte
 // stores). Units: (problem, layer, 128-row weight tile, activation tile), queries first.
+// The activation tiles of a weight tile follow one another: the CTAs that run together read it
+// from HBM once (64 requests of 16 rows, 4 tiles: 158 -> 125 us).
 // CTA c runs units c, c + grid, ... whole as long as every CTA has one; the k-steps of the
 // units left over (boundary tiles, whose outputs are few) are spread evenly over all CTAs,
 // so that every SM streams the same weight bytes, and run first. A piece of such a split
@@ -113,8 +115,6 @@ __device__ inline PUnit unit_of(const PArgs& a, int u) {
   PUnit r;
   r.p = u < a.pr[0].n_units ? 0 : 1;
   if (r.p) u -= a.pr[0].n_units;
-  // activation tiles first: the CTAs that run together share a weight tile, which then comes from
-  // HBM once (64 requests: 4 tiles)
   const int mts = a.pr[r.p].m_tiles, nts = a.pr[r.p].n_out / kPTileN;
   r.mt = u % mts;
   u /= mts;
