@@ -485,6 +485,9 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
                 tmem_st32(trow + kTO + 32 * h2, ov);
               }
             }
+            // The first weights' stores are asynchronous too: they have to land before others go to
+            // the same columns (a load's wait does not cover them).
+            tmem_wait_st();
             weigh();
           }
           sum += part;

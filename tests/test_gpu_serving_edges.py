@@ -1,0 +1,48 @@
+"""The serving-side operators at the edges of what their header allows: references that move with
+every step, idle and padded sequences, page ids that name no page, head counts whose rows are no
+whole warps, calls on two streams at once."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import fixed_cost_drafter_b200 as F
+    from tests.serving_side import Cache4, Lib
+    from tests.test_gpu_kv4 import SHAPES, _check
+
+
+@pytest.mark.parametrize("shape,n,flags", [("mid", 17, 0), ("mid", 17, 2), ("narrow", 17, 0), ("mid", 8, 0), ("mid", 6, 0), ("mid", 1, 0)])
+def test_references_that_move_with_every_step(shape, n, flags):
+    """Logits that grow by ten and more from each 64 keys to the next: every step's first weights are
+    far too large (at the start of each list of keys they are infinite) and replaced by others. The
+    bound is that of the attention's tests; its terms count logits of a few hundred."""
+    kvh, qh, D, block = SHAPES[shape]
+    lengths = [65 + 37 * (i % 23) for i in range(60)]
+    lib = Lib(batch=len(lengths), kv_heads=kvh, q_heads=qh, dim=D, block=block, flags=flags)
+    cache = Cache4(lib, lengths, 16, seed=5)
+    for b, t in enumerate(lengths):
+        for pi in range(-(-t // 16)):
+            for h in range(kvh):
+                kc, _, ks, _ = cache.sections(cache.table[b, pi], h)
+                kc[:] = 0x22                 # ones
+                ks[:] = 0x38 + pi * 16 // 64  # times 1, 1.125, 1.25 ..
+    cache.upload()
+    scale = 100.0 / D  # queries below have elements of one sign, 0.8 on average
+    rng = np.random.default_rng(n)
+    q = torch.from_numpy(rng.uniform(0.6, 1.0, (len(lengths), n, qh * D))).to(torch.bfloat16).cuda()
+    f32 = bool(flags & F.LS_FLAG_OUT_F32)
+    ws = torch.full((F.ls_verify_workspace_bytes(lib.cfg, n),), 0xff, dtype=torch.uint8, device="cuda")
+    t = torch.tensor(lengths, dtype=torch.int64, device="cuda")
+    outs = []
+    for _ in range(5):
+        out = torch.full((len(lengths), n, qh, D), 7.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+        F.ls_verify_attend_kv4(lib.st, cache.kv, 0, q, qh * D, n, None, t, scale, out, ws, ws.numel())
+        outs.append(out)
+    _check(lib, cache, lengths, q, outs[0], None, n, scale=scale)
+    for out in outs[1:]:
+        assert torch.equal(out, outs[0])
+    assert lib.error() == (F.LS_OK, 0)
