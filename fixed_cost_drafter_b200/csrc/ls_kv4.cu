@@ -84,12 +84,13 @@ template <> __device__ inline float top_of<__nv_bfloat16>(const uint4& v) {
   return m >= 0x7f80u ? INFINITY : __uint_as_float(m << 16);
 }
 
-// This thread's row, and its 16 bytes' first element in it.
+// This thread's row, and its 16 bytes' first element in it; false where there is none (rows past
+// the last, and the threads that fill the CTA's last warp).
 __device__ inline bool kv4_place(const Kv4Args& a, int vec, int64_t& row, int& e) {
   const int in_cta = int(threadIdx.x * a.per_row_inv >> 16);  // threadIdx.x / per_row
   row = int64_t(blockIdx.x) * a.per_cta + in_cta;
   e = (int(threadIdx.x) - in_cta * a.per_row) * vec;
-  return row < a.n_rows;
+  return in_cta < a.per_cta && row < a.n_rows;
 }
 
 template <typename T>
@@ -197,12 +198,16 @@ Kv4Args kv4_args(const Dev& p, const ls_paged_kv4& kv, int layer, const int64_t*
   return a;
 }
 
+// Whole warps (at most kKv4Threads): the append's shuffles name every lane of a warp, and rows of 3
+// heads of 64 or of 5 heads of 128, say, end inside one.
+int kv4_threads(const Kv4Args& a) { return (a.per_cta * a.per_row + 31) / 32 * 32; }
+
 }  // namespace
 
 cudaError_t launch_kv4_append(const Dev& p, const ls_paged_kv4& kv, int layer, const void* k, const void* v,
                               int64_t row_stride, const int64_t* slots, int64_t n_rows, cudaStream_t stream) {
   const Kv4Args a = kv4_args(p, kv, layer, slots, n_rows, const_cast<void*>(k), const_cast<void*>(v), row_stride);
-  const int threads = a.per_cta * a.per_row;
+  const int threads = kv4_threads(a);
   const int64_t blocks = (n_rows + a.per_cta - 1) / a.per_cta;
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
   const unsigned grid = static_cast<unsigned>(blocks);
@@ -213,7 +218,7 @@ cudaError_t launch_kv4_append(const Dev& p, const ls_paged_kv4& kv, int layer, c
 cudaError_t launch_kv4_read(const Dev& p, const ls_paged_kv4& kv, int layer, const int64_t* slots, int64_t n_rows,
                             void* k, void* v, int64_t row_stride, cudaStream_t stream) {
   const Kv4Args a = kv4_args(p, kv, layer, slots, n_rows, k, v, row_stride);
-  const int threads = a.per_cta * a.per_row;
+  const int threads = kv4_threads(a);
   const int64_t blocks = (n_rows + a.per_cta - 1) / a.per_cta;
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
   const unsigned grid = static_cast<unsigned>(blocks);

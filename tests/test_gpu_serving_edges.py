@@ -11,6 +11,7 @@ pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     import fixed_cost_drafter_b200 as F
+    import oracle as O
     from tests.serving_side import Cache4, Lib
     from tests.test_gpu_kv4 import SHAPES, _check
 
@@ -45,4 +46,37 @@ def test_references_that_move_with_every_step(shape, n, flags):
     _check(lib, cache, lengths, q, outs[0], None, n, scale=scale)
     for out in outs[1:]:
         assert torch.equal(out, outs[0])
+    assert lib.error() == (F.LS_OK, 0)
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("heads", range(1, 9))
+def test_rows_of_every_head_count(heads, dtype, dim):
+    """Rows of 3, 5, 6 and 7 heads are no whole number of warps: the CTAs' last warps are filled with
+    threads that have no row. Bytes equal the oracle's, and nothing else is written."""
+    n, ps = 83, 16
+    lib = Lib(kv_heads=heads, q_heads=heads, dim=dim, dtype=dtype)
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    k, v = (torch.randn(n, heads * dim, generator=g, device="cuda").to(lib.tdtype) for _ in range(2))
+    pages = -(-n // ps) + 1
+    slots = np.random.default_rng(heads).permutation(pages * ps)[:n]
+    d_slots = torch.from_numpy(slots).cuda()
+    per = F.ls_kv4_page_bytes(lib.cfg, ps)
+    cache = torch.full((pages, per), 0xA5, dtype=torch.uint8, device="cuda")
+    kv = F.make_paged_kv4([cache], per, None, 1, ps, pages)
+    F.ls_kv4_append(lib.st, kv, 0, k, v, heads * dim, d_slots, n)
+    want = np.full((pages, per), 0xA5, np.uint8)
+    back = []
+    for which, x in enumerate((k, v)):
+        c, s = O.kv4_encode(x.double().cpu().numpy().reshape(n, heads, dim))
+        back.append(O.kv4_decode(c, s).reshape(n, heads * dim))
+        for i in range(n):
+            for h in range(heads):
+                sec = O.kv4_sections(want[slots[i] // ps], h, ps, dim)
+                sec[which][slots[i] % ps], sec[2 + which][slots[i] % ps] = c[i, h], s[i, h]
+    assert np.array_equal(cache.cpu().numpy(), want)
+    out = torch.full((2, n + 1, heads * dim), 7.0, dtype=lib.tdtype, device="cuda")
+    F.ls_kv4_read_rows(lib.st, kv, 0, d_slots, n, out[0], out[1], heads * dim)
+    got = out.double().cpu().numpy()
+    assert np.array_equal(got[0, :n], back[0]) and np.array_equal(got[1, :n], back[1]) and (got[:, n] == 7).all()
     assert lib.error() == (F.LS_OK, 0)
