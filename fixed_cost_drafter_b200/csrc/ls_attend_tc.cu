@@ -641,6 +641,10 @@ attend_tc_kernel(const Dev p, const TcArgs a, const __grid_constant__ CUtensorMa
     for (int n = issued > nst ? issued - nst : 0; n < issued; ++n)
       mbar_wait_bounded(&fullb[n % nst], (n / nst) & 1, kWaitLimit);
   }
+  // A launch that waited for nothing still must not complete before the kernel before it: what is
+  // launched next waits for this grid alone, and may write what that kernel reads (the next
+  // projections write the queries of every layer's call) or read what it writes.
+  if (no_wait) grid_dependency_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

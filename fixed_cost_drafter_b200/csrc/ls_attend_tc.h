@@ -28,7 +28,8 @@ enum AttendLaunch : int {
                            // this stream: the first K/V chunks of the views before the wait
                            // (Q and the boundary rows after it)
   kAttendFree = 3          // settled views, and the caller's inputs were complete before the
-                           // kernel before it started (LS_ATTEND_INPUTS_READY): no wait
+                           // kernel before it started (LS_ATTEND_INPUTS_READY): no wait but at
+                           // its end (it completes no earlier than the kernel before it)
 };
 // views: non-zero OR of LS_VIEW_* (the views that take part in the softmax).
 // side_by_side: the caller chains launches that need not wait for one another

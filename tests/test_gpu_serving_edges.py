@@ -80,3 +80,51 @@ def test_rows_of_every_head_count(heads, dtype, dim):
     got = out.double().cpu().numpy()
     assert np.array_equal(got[0, :n], back[0]) and np.array_equal(got[1, :n], back[1]) and (got[:, n] == 7).all()
     assert lib.error() == (F.LS_OK, 0)
+
+
+@pytest.mark.parametrize("adapters", [True, False])
+def test_projections_behind_per_layer_calls_that_do_not_wait(adapters):
+    """Drafting passes back to back: the projections of one write the queries and boundary rows that
+    the attention calls of the pass before, launched with LS_ATTEND_INPUTS_READY, read.
+    Every pass's outputs equal those of the same pass with a synchronisation after each call."""
+    b, layers, kvh, qh, D, hidden, block = 16, 4, 8, 32, 128, 512, 16
+    lib = Lib(batch=b, layers=layers, kv_heads=kvh, q_heads=qh, dim=D, hidden=hidden, block=block)
+    assert F.ls_attend_uses_tensor_cores(lib.st)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    n = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(torch.bfloat16)
+    t = torch.full((b,), 300, dtype=torch.int64, device="cuda")
+    k = n(b, layers, 300, kvh * D)
+    ws = torch.empty(F.ls_prefill_workspace_bytes(lib.cfg, 0, 300), dtype=torch.uint8, device="cuda")
+    F.ls_prefill_summary(lib.st, k, n(b, layers, 300, kvh * D), 300 * kvh * D, kvh * D, t, 0, 300, n(b, layers, hidden), ws, ws.numel())
+    w_kv, w_q = n(layers, 2 * kvh * D, hidden, std=hidden ** -0.5), n(layers, qh * D, hidden, std=hidden ** -0.5)
+    bank = [n(3, layers, 16, hidden, std=hidden ** -0.5), n(3, layers, qh * D, 16), n(3, layers, 16, hidden, std=hidden ** -0.5),
+            n(3, layers, 2 * kvh * D, 16), torch.ones(3, device="cuda"), torch.tensor([i % 4 - 1 for i in range(b)], dtype=torch.int32, device="cuda")]
+    lora = F.make_lora(3, 16, *bank)
+    lws = torch.empty(F.ls_lora_workspace_bytes(lib.cfg, 16), dtype=torch.uint8, device="cuda")
+    xs = [n(b, layers, block, hidden) for _ in range(6)]
+    bkv = torch.empty(b, layers, 2 * kvh * D, dtype=torch.bfloat16, device="cuda")
+    q = torch.empty(b, layers, block, qh * D, dtype=torch.bfloat16, device="cuda")
+    hint = F.LS_VIEW_ALL | F.LS_ATTEND_INPUTS_READY
+
+    def run(sync):
+        outs = torch.full((len(xs), layers, b, layers, block, qh, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        for i, x in enumerate(xs):
+            if adapters:
+                F.ls_draft_prologue_lora(lib.st, w_kv, w_q, x, lora, bkv, q, lws, lws.numel())
+            else:
+                F.ls_draft_prologue(lib.st, w_kv, w_q, x, bkv, q)
+            if sync:
+                torch.cuda.synchronize()
+            for c in range(layers):  # all but the first wait for nothing
+                F.ls_draft_attend_views(lib.st, 0, layers, q, bkv, bkv[:, :, kvh * D:], 2 * kvh * D, D ** -0.5,
+                                        F.LS_VIEW_ALL if c == 0 else hint, outs[i, c])
+                if sync:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+
+    want = run(True)
+    for _ in range(5):
+        assert torch.equal(run(False), want)
+    assert lib.error() == (F.LS_OK, 0)
