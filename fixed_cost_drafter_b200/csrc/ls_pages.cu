@@ -5,7 +5,7 @@
 // need over the sequences before b, sequence b's j-th new page is free[count - 1 - before_b - j]
 // (a stack popped in the order of the sequences), and row i of it has slot
 // table[b][(len + i) / ps] * ps + (len + i) mod ps. Trim pushes the pages behind ceil(len / ps)
-// so that it undoes an extend entry for entry.
+// so that it undoes an extend entry for entry; entries that name no page are left out.
 //
 // One launch each. Every CTA of a sequence sums what it needs over the sequences before it
 // itself (a few loads per thread from L2, instead of a scan kernel before this one), takes new
@@ -303,7 +303,24 @@ __global__ void __launch_bounds__(kPagesThreads) pages_trim_kernel(const PagesAr
     const SeqPlan s = plan_trim(a, i);
     if (s.pages > 0) a.pool.held[i] = s.held - s.pages;
   }
-  if (tid == 0) *a.pool.free_count = count + int(total);
+  // Ids that name no page are dropped, or a later extend would hand them to other sequences: where the
+  // error word tells of one (of this call or before it), this CTA closes the gaps. Each step's entries
+  // are read before any of its places, which lie at or before them, is written (block_scan meets).
+  int64_t kept = total;
+  __threadfence();
+  // (one thread asks for all: a call on another stream may set the bit meanwhile)
+  if (__syncthreads_or(tid == 0 && (*reinterpret_cast<volatile int32_t*>(a.err) & LS_DEVERR_PAGE))) {
+    kept = 0;
+    for (int64_t i0 = 0; i0 < total; i0 += kPagesThreads) {
+      const int32_t id = i0 + tid < total ? __ldcg(a.pool.free_pages + count + i0 + tid) : -1;
+      const bool real = id >= 0 && id < a.pool.num_pages;
+      int64_t all;
+      const int64_t at = kept + block_scan(real, &all);
+      if (real) a.pool.free_pages[count + at] = id;
+      kept += all;
+    }
+  }
+  if (tid == 0) *a.pool.free_count = count + int(kept);
 }
 
 PagesArgs pages_args(const Dev& p, const ls_page_pool& pool, const int64_t* len) {

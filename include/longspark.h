@@ -460,7 +460,9 @@ LS_API int ls_pages_extend(ls_state* st, const ls_page_pool* h_pool, const int64
  * an extend and a trim to the lengths before it leave the list as it was. A negative length
  * or a held count outside [0, max_blocks] sets LS_DEVERR_ROWS and the sequence keeps its
  * pages. When the list would hold more than num_pages, or *free_count is outside
- * [0, num_pages], LS_DEVERR_POOL is set and nothing changes.                              */
+ * [0, num_pages], LS_DEVERR_POOL is set and nothing changes. A page id outside
+ * [0, num_pages) among the entries behind sets LS_DEVERR_PAGE and is not returned: the list
+ * gets the others, as if it had not been there.                                           */
 LS_API int ls_pages_trim(ls_state* st, const ls_page_pool* h_pool, const int64_t* d_len, cudaStream_t stream);
 
 /* ---- a paged KV cache held in 4 bits -------------------------------------------------

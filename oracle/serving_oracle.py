@@ -67,13 +67,15 @@ def pages_trim(table, held, free, count, length, page_size, num_pages):
     order = [x for s in back for x in s]
     if count < 0 or count + len(order) > num_pages:
         return count, flags | {"pool"}
-    for at, (b, j) in enumerate(order):  # the first one ends up on top of the stack
-        if not 0 <= table[b, j] < num_pages:
-            flags.add("page")
-        free[count + len(order) - 1 - at] = table[b, j]
+    real = [(b, j) for b, j in order if 0 <= table[b, j] < num_pages]
+    if len(real) < len(order):  # ids that name no page are dropped
+        flags.add("page")
+    for at, (b, j) in enumerate(real):  # the first one ends up on top of the stack
+        free[count + len(real) - 1 - at] = table[b, j]
+    for b, j in order:
         table[b, j] = -1
         held[b] -= 1
-    return count + len(order), flags
+    return count + len(real), flags
 
 
 # ---- the 4-bit format -----------------------------------------------------------------------

@@ -128,3 +128,45 @@ def test_projections_behind_per_layer_calls_that_do_not_wait(adapters):
     for _ in range(5):
         assert torch.equal(run(False), want)
     assert lib.error() == (F.LS_OK, 0)
+
+
+@pytest.mark.parametrize("b,ps,pages_each", [(3, 16, 7), (64, 8, 90), (2, 16, 3000)])
+def test_trim_leaves_out_ids_that_name_no_page(b, ps, pages_each):
+    """Ids outside the pool among a table's returned entries are flagged and dropped: a later extend
+    hands out real pages only, and takes and returns them as ever while the error word still tells."""
+    rng = np.random.default_rng(b)
+    num = b * pages_each + 9
+    lib = Lib(batch=b)
+    ids = rng.permutation(num).astype(np.int32)
+    free, table = ids[:9], ids[9:].reshape(b, pages_each).copy()
+    for bad in (num, -1, 1 << 30, -(1 << 31)):
+        table[rng.integers(0, b), rng.integers(0, pages_each)] = bad
+    table[0, 0] = table[0, -1] = num + 5
+    keep = rng.integers(0, 3, b)
+    keep[0] = 0
+    d_table, d_held, d_count = (torch.from_numpy(x).cuda() for x in (table, np.full(b, pages_each, np.int32), np.array([9], np.int32)))
+    d_free = torch.from_numpy(np.concatenate([free, np.full(num - 9, -9, np.int32)])).cuda()
+    pool = F.make_page_pool(d_table, d_held, d_free, d_count, pages_each, ps, num)
+    length = torch.from_numpy(keep * ps).cuda()
+    gone = np.concatenate([table[i, keep[i]:] for i in range(b)])
+    back = gone[(gone >= 0) & (gone < num)]
+    want_free = list(free) + list(back[::-1])
+    want_table = np.where(np.arange(pages_each) < keep[:, None], table, -1)
+
+    def check():
+        assert d_count.tolist() == [len(want_free)] and d_held.tolist() == keep.tolist()
+        assert d_free[:len(want_free)].tolist() == want_free and np.array_equal(d_table.cpu().numpy(), want_table)
+
+    F.ls_pages_trim(lib.st, pool, length)
+    assert lib.error()[1] == F.LS_DEVERR_PAGE
+    check()
+    slots = torch.full((b, 2 * ps), -7, dtype=torch.int64, device="cuda")
+    for clear in (False, True):
+        if clear:
+            lib.clear()
+        F.ls_pages_extend(lib.st, pool, length, None, 2 * ps, None, slots, slots.numel())
+        taken = want_free[::-1][:2 * b]
+        assert (slots.view(b * 2, ps)[:, 0] // ps).tolist() == taken
+        F.ls_pages_trim(lib.st, pool, length)
+        check()
+    assert lib.error() == (F.LS_OK, 0)
