@@ -52,7 +52,10 @@ __device__ inline int ver_rows(const VerArgs& a, int b) {
   const int n = a.rows[b];
   return n < 0 ? 0 : (n > a.n_rows ? a.n_rows : n);
 }
-__device__ inline int64_t ver_chunks(const VerArgs& a, int b) { return (ver_len(a, b) + kVerChunk - 1) / kVerChunk; }
+// (a sequence without query rows, an idle place of a padded batch, has no work, however long it is)
+__device__ inline int64_t ver_chunks(const VerArgs& a, int b) {
+  return ver_rows(a, b) > 0 ? (ver_len(a, b) + kVerChunk - 1) / kVerChunk : 0;
+}
 
 __device__ inline int64_t ver_warp_sum(int64_t x) {
 #pragma unroll
@@ -118,7 +121,7 @@ __device__ inline bool ver_next(const VerArgs& a, VerCursor& u, VerPiece& p) {
   if (u.left <= 0) return false;
   while (u.b < a.b) {
     p.len = ver_len(a, u.b);
-    p.n = (p.len + kVerChunk - 1) / kVerChunk;
+    p.n = ver_chunks(a, u.b);
     if (p.n > 0) break;
     ++u.b;
   }

@@ -520,7 +520,8 @@ LS_API size_t ls_verify_workspace_bytes(const ls_config* cfg, int32_t n_rows);
  *   d_q         `dtype`, element (b, i, qh, d) at [(b * n_rows + i) * q_stride + qh * D + d];
  *               q_stride >= Hq*D, a multiple of 8.
  *   d_rows      int32 [b]: query rows of sequence b (0 .. n_rows), or NULL: n_rows each.
- *               Output rows i >= rows[b] stay as they were.
+ *               Output rows i >= rows[b] stay as they were; of a sequence with 0 rows (an idle
+ *               place of a padded batch) no page is read.
  *   d_kv_len    int64 [b]: cached rows of sequence b, the query rows' own included (they are
  *               appended before this call): query row i stands at position
  *               kv_len - rows + i and sees positions 0 .. that one. A row that stands before

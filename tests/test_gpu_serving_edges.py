@@ -13,7 +13,7 @@ if torch.cuda.is_available():
     import fixed_cost_drafter_b200 as F
     import oracle as O
     from tests.serving_side import Cache4, Lib
-    from tests.test_gpu_kv4 import SHAPES, _check
+    from tests.test_gpu_kv4 import SHAPES, _attend, _check
 
 
 @pytest.mark.parametrize("shape,n,flags", [("mid", 17, 0), ("mid", 17, 2), ("narrow", 17, 0), ("mid", 8, 0), ("mid", 6, 0), ("mid", 1, 0)])
@@ -170,3 +170,24 @@ def test_trim_leaves_out_ids_that_name_no_page(b, ps, pages_each):
         F.ls_pages_trim(lib.st, pool, length)
         check()
     assert lib.error() == (F.LS_OK, 0)
+
+
+@pytest.mark.parametrize("shape,n,flags", [("mid", 1, 0), ("mid", 5, 0), ("mid", 17, 0), ("narrow", 17, 0), ("mid", 17, 1)])
+def test_sequences_without_rows_are_not_read(shape, n, flags):
+    """The idle slots of a padded batch: their lengths are in range, their tables name no pages.
+    Nothing of them is read, so nothing is flagged; the others' outputs are what they are alone."""
+    kvh, qh, D, block = SHAPES[shape]
+    lengths, rows = [300, 5000, 64, 40, 2000], [n, 0, n, 0, 0]
+    lib = Lib(batch=5, kv_heads=kvh, q_heads=qh, dim=D, block=block, flags=flags)
+    cache = Cache4(lib, lengths, 16, seed=9)
+    cache.table[[1, 3, 4]] = -1
+    cache.upload()
+    q, out = _attend(lib, cache, lengths, n, rows=rows)
+    assert lib.error() == (F.LS_OK, 0)
+    _check(lib, cache, [300, 0, 64, 0, 0], q, out, rows, n)
+    assert (out[[1, 3, 4]] == 7).all()
+    _, bad = _attend(lib, cache, [300, -1, 64, 40, 2000], n, rows=rows)  # a length out of range still is
+    assert lib.error()[1] == F.LS_DEVERR_PREFIX_LEN and torch.equal(bad, out)
+    lib.clear()
+    _, none = _attend(lib, cache, lengths, n, rows=[0] * 5)
+    assert (none == 7).all() and lib.error() == (F.LS_OK, 0)
