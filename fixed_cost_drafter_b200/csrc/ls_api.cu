@@ -160,11 +160,11 @@ bool kv4_shapes_ok(const ls_config& c, int page_size) {
   return (c.head_dim == 64 || c.head_dim == 128) && pow2(page_size) && page_size >= 16 && page_size <= 256;
 }
 
-// A 4-bit cache usable by the kernels for this config, and its layer `layer`.
+// A 4-bit cache usable by the kernels for this config, and its layer `layer` (one of the target's:
+// more than the n_layers that the drafter taps).
 int validate_kv4(const ls_config& c, const ls_paged_kv4* kv, int layer, bool table) {
   if (!kv) return LS_ERR_INVALID_ARG;
-  if (c.n_layers > LS_MAX_PAGED_LAYERS) return LS_ERR_UNSUPPORTED;
-  if (layer < 0 || layer >= c.n_layers) return LS_ERR_INVALID_ARG;
+  if (layer < 0 || layer >= LS_MAX_PAGED_LAYERS) return LS_ERR_INVALID_ARG;
   if (!kv->layers[layer] || !aligned16(kv->layers[layer])) return LS_ERR_INVALID_ARG;
   if (kv->page_size < 1 || kv->num_pages < 1) return LS_ERR_INVALID_ARG;
   if (table && (!kv->block_table || !aligned(kv->block_table, 4) || kv->max_blocks < 1)) return LS_ERR_INVALID_ARG;

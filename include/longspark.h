@@ -473,7 +473,10 @@ LS_API int ls_pages_trim(ls_state* st, const ls_page_pool* h_pool, const int64_t
  * it reads as NaN.
  * Host struct, passed by pointer; the pointers in it are DEVICE memory owned by the caller.
  *   layers[l]   base of the target's layer l: page p at layers[l] + p * page_stride (bytes;
- *               16-byte aligned, page_stride a multiple of 16 and >= ls_kv4_page_bytes).
+ *               16-byte aligned, page_stride a multiple of 16 and >= ls_kv4_page_bytes). All of
+ *               the target's layers, not the tapped ones alone: a call's `layer` is any l <
+ *               LS_MAX_PAGED_LAYERS whose base is given (of a deeper target, further descriptors
+ *               hold the rest); NULL where there is none.
  *   A page holds, for each KV head in turn, page_size * 9 D / 8 bytes:
  *               K codes [page_size][D/2], V codes [page_size][D/2], K scales
  *               [page_size][D/16], V scales [page_size][D/16]; byte i of a row's codes holds

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
     import fixed_cost_drafter_b200 as F
     import oracle as O
-    from tests.serving_side import Cache4, Lib
+    from tests.serving_side import Cache4, Lib, refused
     from tests.test_gpu_kv4 import SHAPES, _attend, _check
 
 
@@ -191,3 +191,36 @@ def test_sequences_without_rows_are_not_read(shape, n, flags):
     lib.clear()
     _, none = _attend(lib, cache, lengths, n, rows=[0] * 5)
     assert (none == 7).all() and lib.error() == (F.LS_OK, 0)
+
+
+@pytest.mark.parametrize("n", [1, 17])
+def test_layers_of_the_target_beyond_the_tapped_ones(n):
+    """The 4-bit cache is the target's: its layers are more than those the drafter taps. Layers the
+    descriptor does not have are refused."""
+    lib = Lib(batch=2, layers=2)
+    lengths, layer = [200, 37], 40
+    cache = Cache4(lib, lengths, 16, seed=3)
+    q, want = _attend(lib, cache, lengths, n)
+    per = F.ls_kv4_page_bytes(lib.cfg, 16)
+    copy = torch.zeros_like(cache.dev)
+    kv = F.make_paged_kv4([None] * layer + [copy], cache.stride, cache.d_table, cache.mb, 16, cache.pages)
+    # rows written and read there are those of layer 0 of a like cache
+    k, v = (torch.randn(50, 256, device="cuda").to(torch.bfloat16) for _ in range(2))
+    slots = torch.arange(50, device="cuda") + 7
+    ref, got = torch.zeros_like(copy), torch.empty(4, 50, 256, dtype=torch.bfloat16, device="cuda")
+    kv0 = F.make_paged_kv4([ref], cache.stride, None, 1, 16, cache.pages)
+    for i, (d, l) in enumerate(((kv0, 0), (kv, layer))):
+        F.ls_kv4_append(lib.st, d, l, k, v, 256, slots, 50)
+        F.ls_kv4_read_rows(lib.st, d, l, slots, 50, got[2 * i], got[2 * i + 1], 256)
+    assert torch.equal(copy, ref) and torch.equal(got[2:], got[:2]) and ref.any()
+    out = torch.full_like(want, 7.0)
+    ws = torch.empty(F.ls_verify_workspace_bytes(lib.cfg, n), dtype=torch.uint8, device="cuda")
+    copy[:, :per] = cache.dev[:, :per]
+    t = torch.tensor(lengths, dtype=torch.int64, device="cuda")
+    args = (q, q.stride(1), n, None, t, 128 ** -0.5, out, ws, ws.numel())
+    F.ls_verify_attend_kv4(lib.st, kv, layer, *args)
+    assert torch.equal(out, want) and lib.error() == (F.LS_OK, 0)
+    for bad in (0, layer - 1, layer + 1, 64, 1 << 30, -1):
+        refused(F.LS_ERR_INVALID_ARG, F.ls_verify_attend_kv4, lib.st, kv, bad, *args)
+        refused(F.LS_ERR_INVALID_ARG, F.ls_kv4_append, lib.st, kv, bad, k, v, 256, slots, 16)
+        refused(F.LS_ERR_INVALID_ARG, F.ls_kv4_read_rows, lib.st, kv, bad, slots, 16, k, v, 256)
