@@ -224,3 +224,90 @@ def test_layers_of_the_target_beyond_the_tapped_ones(n):
         refused(F.LS_ERR_INVALID_ARG, F.ls_verify_attend_kv4, lib.st, kv, bad, *args)
         refused(F.LS_ERR_INVALID_ARG, F.ls_kv4_append, lib.st, kv, bad, k, v, 256, slots, 16)
         refused(F.LS_ERR_INVALID_ARG, F.ls_kv4_read_rows, lib.st, kv, bad, slots, 16, k, v, 256)
+
+
+def test_adapters_of_two_states_on_two_streams():
+    """Calls that overlap on the GPU, with a state and a workspace each; the next round's ids and
+    inputs written on each call's own stream right before it."""
+    from tests.test_gpu_lora import Case
+    ids = [[0, 1, 2, -1, 2, 0], [2, -1, 0, 0, 1, 1]]
+    cases = [Case(6, 16, 2, 1024, 64, 3, ids[s], seed=20 + s) for s in range(2)]
+    sets = []
+    for c in cases:
+        xs = [c.x.clone(), -c.x, c.x.flip(0)]
+        whiches = [c.which.clone(), c.which.flip(0), c.which.roll(1)]
+        want = []
+        for x, w in zip(xs, whiches):
+            c.x.copy_(x)
+            c.which.copy_(w)
+            torch.cuda.synchronize()
+            want.append(c.run())
+            torch.cuda.synchronize()
+        c.check(*want[-1])
+        sets.append((c, xs, whiches, want, torch.cuda.Stream(), [c.outputs() for _ in range(12)]))
+    torch.cuda.synchronize()
+    for i in range(12):
+        for c, xs, whiches, want, stream, outs in sets:
+            with torch.cuda.stream(stream):
+                c.x.copy_(xs[i % 3])
+                c.which.copy_(whiches[i % 3])
+                F.ls_draft_prologue_lora(c.lib.st, c.w_kv, c.w_q, c.x, c.desc, *outs[i], c.ws, c.ws.numel())
+    torch.cuda.synchronize()
+    for c, xs, whiches, want, stream, outs in sets:
+        for i, got in enumerate(outs):
+            assert torch.equal(got[0], want[i % 3][0]) and torch.equal(got[1], want[i % 3][1]), i
+        assert c.lib.error() == (F.LS_OK, 0)
+
+
+def test_ids_and_weights_written_before_every_call():
+    """Ids and weights that the kernels right before each call write, every call's outputs compared
+    with those of the same values settled long before."""
+    from tests.test_gpu_lora import Case
+    c = Case(16, 16, 1, 1024, 16, 4, [0] * 16, seed=7)
+    whiches = [torch.tensor([(i * s) % 5 - 1 for i in range(16)], dtype=torch.int32, device="cuda") for s in (3, 2)]
+    banks = [[t.clone() for t in (c.a_q, c.b_q, c.a_kv, c.b_kv, c.scale)], [-c.a_q, c.b_q * 2, -c.a_kv, c.b_kv * 0.5, c.scale + 1]]
+
+    def put(s):
+        c.which.copy_(whiches[s])
+        for t, v in zip((c.a_q, c.b_q, c.a_kv, c.b_kv, c.scale), banks[s]):
+            t.copy_(v)
+
+    want = []
+    for s in range(2):
+        put(s)
+        torch.cuda.synchronize()
+        want.append(c.run())
+        torch.cuda.synchronize()
+        c.check(*want[s])
+    assert not torch.equal(want[0][1], want[1][1])
+    got = []
+    for i in range(40):
+        put(i % 2)
+        got.append(c.run())
+    for i, (bkv, q) in enumerate(got):
+        assert torch.equal(bkv, want[i % 2][0]) and torch.equal(q, want[i % 2][1]), i
+    assert c.lib.error() == (F.LS_OK, 0)
+
+
+@pytest.mark.parametrize("n", [1, 6, 17])
+def test_repeated_calls_from_fresh_states_give_the_same_bits(n):
+    """Work that is split over CTAs and joined: other states, other workspaces with other contents and
+    other calls beside them change no bit of the outputs."""
+    lengths = [3000, 1, 517, 0, 9000]
+    outs = []
+    for r in range(4):
+        lib = Lib(batch=5, kv_heads=8, q_heads=32)
+        cache = Cache4(lib, lengths, 16, seed=6)
+        q, out = _attend(lib, cache, lengths, n, seed=2)
+        noise = torch.randn(1 << 24, device="cuda")
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                noise.mul_(1.0001)
+        outs.append(out)
+        outs.append(_attend(lib, cache, lengths, n, seed=2)[1])
+        torch.cuda.synchronize()
+        assert lib.error() == (F.LS_OK, 0)
+    for out in outs[1:]:
+        assert torch.equal(out, outs[0])
