@@ -135,17 +135,22 @@ __device__ inline int64_t block_scan(int64_t x, int64_t* total) {
   return base + inc - x;
 }
 
-// True in every thread of the last CTA to arrive: every other CTA has read what it needs.
-__device__ inline bool last_to_arrive(const PagesArgs& a) {
-  __shared__ int last;
-  __syncthreads();
+// True in every thread of the last CTA to arrive: every other CTA has read what it needs. `any`
+// becomes whether `mine` was set in a thread of one of them, told by a bit of the count (a grid
+// has fewer than 2^30 CTAs): reading the error word for it would cost a trip more.
+constexpr int32_t kArriveMark = 1 << 30;
+__device__ inline bool last_to_arrive(const PagesArgs& a, bool mine, bool& any) {
+  __shared__ int32_t before;
+  const bool mark = __syncthreads_or(mine);
   if (threadIdx.x == 0) {
     __threadfence();
-    last = atomicAdd(a.arrive, 1) == int(gridDim.x) - 1;
-    if (last) *a.arrive = 0;  // zero again for the next call
+    if (mark) atomicOr(a.arrive, kArriveMark);
+    before = atomicAdd(a.arrive, 1);
+    if ((before & ~kArriveMark) == int(gridDim.x) - 1) *a.arrive = 0;  // zero again for the next call
   }
   __syncthreads();
-  return last != 0;
+  any = (before & kArriveMark) != 0;
+  return (before & ~kArriveMark) == int(gridDim.x) - 1;
 }
 
 __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const PagesArgs a) {
@@ -234,7 +239,8 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
     if (seq == a.b - 1) a.row_begin[a.b] = first_row + me.n;
   }
   if (bits) set_err(a.err, bits);
-  if (!last_to_arrive(a)) return;
+  bool unused;
+  if (!last_to_arrive(a, false, unused)) return;
 
   int64_t taken = 0;  // pages given so far, and pages needed so far
   int64_t needed = 0;
@@ -298,18 +304,18 @@ __global__ void __launch_bounds__(kPagesThreads) pages_trim_kernel(const PagesAr
     }
   }
   if (bits) set_err(a.err, bits);
-  if (!last_to_arrive(a) || !ok) return;
+  bool gaps;  // a CTA met an id that names no page
+  if (!last_to_arrive(a, bits & LS_DEVERR_PAGE, gaps) || !ok) return;
   for (int i = tid; i < a.b; i += kPagesThreads) {
     const SeqPlan s = plan_trim(a, i);
     if (s.pages > 0) a.pool.held[i] = s.held - s.pages;
   }
-  // Ids that name no page are dropped, or a later extend would hand them to other sequences: where the
-  // error word tells of one (of this call or before it), this CTA closes the gaps. Each step's entries
-  // are read before any of its places, which lie at or before them, is written (block_scan meets).
+  // Such ids are dropped, or a later extend would hand them to other sequences: this CTA closes the
+  // gaps. Each step's entries are read before any of its places, which lie at or before them, is
+  // written (block_scan meets).
   int64_t kept = total;
-  __threadfence();
-  // (one thread asks for all: a call on another stream may set the bit meanwhile)
-  if (__syncthreads_or(tid == 0 && (*reinterpret_cast<volatile int32_t*>(a.err) & LS_DEVERR_PAGE))) {
+  if (gaps) {
+    __threadfence();
     kept = 0;
     for (int64_t i0 = 0; i0 < total; i0 += kPagesThreads) {
       const int32_t id = i0 + tid < total ? __ldcg(a.pool.free_pages + count + i0 + tid) : -1;
