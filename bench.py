@@ -741,12 +741,51 @@ def run_gpu(args):
                 for name in configs:
                     cwl = WLM.CONFIGS[name]
                     configs[name]["cpu_oracle"] = cpu_record(cwl, *oracle_timing(name, 1, budget_s=args.cpu_budget / 3))
-        print(json.dumps(line))
+        if args.details:
+            with open(args.details, "w", encoding="utf-8") as f:
+                json.dump(line, f)
+        print(json.dumps(short_line(line)))
     run.close()
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
     return 0
+
+
+def short_line(line):
+    """The record as it is printed: one line of less than five thousand characters, which whoever reads
+    the end of a log gets whole (with the sweep's points it had 28 thousand). Of the parts beside the
+    headline it keeps the figures, and --details writes everything to a file; numbers keep six
+    digits, `value` and `ms_per_step` all of theirs."""
+    def six(x):
+        if isinstance(x, float):
+            return int(x) if x.is_integer() else float(f"{x:.6g}")
+        if isinstance(x, dict):
+            return {k: six(v) for k, v in x.items()}
+        return [six(v) for v in x] if isinstance(x, (list, tuple)) else x
+
+    out = {k: v if k in ("value", "ms_per_step") else six(v) for k, v in line.items()}
+
+    def shorten(key, f):
+        if out.get(key):
+            out[key] = f(out[key])
+
+    shorten("sweep", lambda x: {"points": len(x["points"]), "flatness_max": max(x["flatness"].values()),
+                                **{k: v for k, v in x.items() if k not in ("points", "flatness")}})
+    shorten("configs", lambda x: {name: {"rounds_per_s": c["rounds_per_s"], "us_per_round": c["us_per_round"]["mean"],
+                                         "round_frac": c["round_frac"], "prefill_ms": c["prefill"]["ms"],
+                                         "cpu_oracle": c.get("cpu_oracle", {}).get("value")} for name, c in x.items()})
+    shorten("drafting_round", lambda x: {
+        "us_per_round": x["us_per_round"], "rounds": x["rounds"], "bytes": x["bytes"], "frac": x["frac"],
+        "split": {k: v for k, v in x["split"].items() if k != "note"},
+        "over_prefix": {k: v for k, v in (x.get("over_prefix") or {}).items() if k != "split"}})
+    shorten("view_ablations", lambda x: {name: v["attend_us"] for name, v in x.items()})
+    shorten("other_output_dtype", lambda x: {"out_dtype": x["out_dtype"], "us_per_round": x["us_per_round"]["mean"],
+                                             "attend_us": x["attend_us"]["mean"]})
+    shorten("paged", lambda x: {"page_size": x["page_size"], "prefill": x["prefill"], "round_us": x["round_us"],
+                                "round_slots_us": (x.get("round_slots_us") or {}).get("mean")})
+    shorten("cpu_baseline", lambda x: {**x, "one_core": x["one_core"]["value"]} if isinstance(x.get("one_core"), dict) else x)
+    return out
 
 
 QWEN3_VOCAB = 151936
@@ -1290,6 +1329,7 @@ def main(argv=None):
     ap.add_argument("--no-configs", action="store_true", help="skip the other workload configurations")
     ap.add_argument("--no-drafting-round", action="store_true",
                     help="skip the drafting round with sampled acceptance and projections")
+    ap.add_argument("--details", default=None, help="write the whole record (the sweep's points among it) to this file")
     ap.add_argument("--prefix", type=int, default=0, help="override the workload's prefix length")
     ap.add_argument("--out", default="bf16", choices=["bf16", "f32"], help="dtype of the attention output")
     args = ap.parse_args(argv)
