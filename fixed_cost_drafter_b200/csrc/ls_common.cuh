@@ -304,7 +304,8 @@ __device__ inline const char* paged_slot(const ls_paged_kv& kv, const char* base
 }
 
 // A launch that may start while the kernel before it on the stream still runs: the kernel waits for
-// it (grid_dependency_wait) before it reads or writes anything, then lets its own successor start.
+// it (grid_dependency_wait) before it reads or writes anything (but for what its own comment names),
+// then lets its own successor start.
 template <typename... A>
 inline cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};

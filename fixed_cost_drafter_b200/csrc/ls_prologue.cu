@@ -824,16 +824,7 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
     const cuuint32_t wbox[2] = {kPKStep, kPTileN}, xbox[2] = {kPKStep, cuuint32_t(2 * Q.pitch)};
     if (!encode_bf16(const_cast<void*>(lora->b_q), 2, wd, str, wbox, &mwl)) return cudaErrorInvalidValue;
     if (!encode_bf16(low, 2, xd, str, xbox, &mxl)) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t lc{};
     const int tiles = lora->rank <= 8 ? 1 : (lora->rank <= 16 ? 2 : 4);  // (x is read again for each 32 of the rank)
-    lc.gridDim = dim3(p.b * p.L, (lora->rank + 8 * tiles - 1) / (8 * tiles) + 1);
-    lc.blockDim = dim3(low_warps(tiles) * 32);
-    lc.stream = stream;
-    cudaLaunchAttribute la[1];
-    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    la[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = la;
-    lc.numAttrs = 1;
     const bool two = p.B > 16;
     const bool wide = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(lora->a_q) |
                         reinterpret_cast<uintptr_t>(lora->a_kv)) & 31) == 0;  // (rows are whole 128 bytes, the boundary view is aligned)
@@ -844,9 +835,9 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
                           : (two ? lora_low_kernel<2, 4, kWide> : lora_low_kernel<1, 4, kWide>);
     };
     const auto low_kernel = wide ? pick(std::true_type{}) : pick(std::false_type{});
-    e = cudaLaunchKernelEx(&lc, low_kernel, pl,
-                           static_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(p.boundary),
-                           p.L, p.B, p.hidden, K.n_out, p.err);
+    e = launch_overlapped(low_kernel, dim3(p.b * p.L, (lora->rank + 8 * tiles - 1) / (8 * tiles) + 1), low_warps(tiles) * 32, 0, stream,
+                          pl, static_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(p.boundary), p.L, p.B,
+                          p.hidden, K.n_out, p.err);
     if (e != cudaSuccess) return e;
   }
   int grid = sms < kProMaxGrid ? sms : kProMaxGrid;
@@ -864,17 +855,7 @@ cudaError_t launch_prologue(const Dev& p, const void* w_kv, const void* w_q, con
   a.rem_steps = split ? rem * a.k_steps : 0;
   a.part = p.pro_part;
   a.count = p.pro_count;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kPThreads);
-  cfg.dynamicSmemBytes = kPSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, pl, mw0, mx0, mw1, mx1, mwl, mxl);
+  return launch_overlapped(kernel, dim3(grid), kPThreads, kPSmemBytes, stream, a, pl, mw0, mx0, mw1, mx1, mwl, mxl);
 }
 
 }  // namespace ls

@@ -168,6 +168,18 @@ __device__ inline const unsigned char* ver_block(const VerArgs& a, int b, int64_
 constexpr int kVerNone = 0x7fffffff;
 __device__ inline bool nan_scale(uint32_t byte) { return (byte & 0x7fu) == 0x7fu; }
 
+// Two values as fp16, low half first; 2^x (of the tensor-core kernels' softmax).
+__device__ inline uint32_t ver_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ inline float ver_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // N output elements to memory, N a multiple of 2.
 template <int N>
 __device__ inline void ver_store(const VerArgs& a, int64_t at, const float* v) {

@@ -57,16 +57,6 @@ __device__ inline uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ inline uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ inline float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ inline void consumers_meet() { asm volatile("bar.sync 1, %0;" ::"n"(kMWarps * 32) : "memory"); }
 
 template <int NT, int D>
@@ -133,8 +123,8 @@ __global__ void __launch_bounds__(kMThreads) verify_mma_kernel(const VerArgs a) 
       const float down = ex == 127 ? 0x1p-127f : __uint_as_float(uint32_t(127 - ex) << 23);
 #pragma unroll
       for (int st = 0; st < kSteps; ++st) {
-        q[nt][st][0] = pack_f16(x[4 * st] * down, x[4 * st + 1] * down);
-        q[nt][st][1] = pack_f16(x[4 * st + 2] * down, x[4 * st + 3] * down);
+        q[nt][st][0] = ver_half2(x[4 * st] * down, x[4 * st + 1] * down);
+        q[nt][st][1] = ver_half2(x[4 * st + 2] * down, x[4 * st + 3] * down);
       }
       const float up = ldexpf(a.scale_log2, ex);
       f[nt][0] = __shfl_sync(0xffffffffu, up, (2 * t) * 4);
@@ -226,7 +216,7 @@ __global__ void __launch_bounds__(kMThreads) verify_mma_kernel(const VerArgs a) 
 #pragma unroll
               for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
               const float nref = fmaxf(ref[nt][e], mx - kMRoom);
-              const float al = ref[nt][e] == nref ? 1.f : exp2_approx(ref[nt][e] - nref);
+              const float al = ref[nt][e] == nref ? 1.f : ver_exp2(ref[nt][e] - nref);
               ref[nt][e] = nref;
               sum[nt][e] *= al;
 #pragma unroll
@@ -239,11 +229,11 @@ __global__ void __launch_bounds__(kMThreads) verify_mma_kernel(const VerArgs a) 
             for (int e = 0; e < 4; ++e) y[e] = seen[e] ? fmaf(x[nt][e], f[nt][e & 1], -ref[nt][e & 1]) : -INFINITY;
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = exp2_approx(y[e]);
+          for (int e = 0; e < 4; ++e) y[e] = ver_exp2(y[e]);
           sum[nt][0] += y[0] + y[2];
           sum[nt][1] += y[1] + y[3];
-          pt[nt][0] = transpose8(pack_f16(y[0], y[1]));  // row g, keys 2 t, 2 t + 1
-          pt[nt][1] = transpose8(pack_f16(y[2], y[3]));  // keys 2 t + 8, 2 t + 9
+          pt[nt][0] = transpose8(ver_half2(y[0], y[1]));  // row g, keys 2 t, 2 t + 1
+          pt[nt][1] = transpose8(ver_half2(y[2], y[3]));  // keys 2 t + 8, 2 t + 9
         }
         // ---- O^T += V^T P^T
         {
@@ -321,7 +311,7 @@ __global__ void __launch_bounds__(kMThreads) verify_mma_kernel(const VerArgs a) 
             float top = s.ref[0][n];
 #pragma unroll
             for (int v = 1; v < kMWarps; ++v) top = fmaxf(top, s.ref[v][n]);
-            const float al = ref[nt][e] == top ? 1.f : exp2_approx(ref[nt][e] - top);
+            const float al = ref[nt][e] == top ? 1.f : ver_exp2(ref[nt][e] - top);
 #pragma unroll
             for (int j = 0; j < kTiles; ++j) {
               float2* dst = reinterpret_cast<float2*>(&s.o[n][g * (D / 8) + 2 * j]);
@@ -347,7 +337,7 @@ __global__ void __launch_bounds__(kMThreads) verify_mma_kernel(const VerArgs a) 
       for (int v = 1; v < kMWarps; ++v) top = fmaxf(top, s.ref[v][n]);
 #pragma unroll
       for (int v = 0; v < kMWarps; ++v)
-        total += s.ref[v][n] == top ? s.sum[v][n] : s.sum[v][n] * exp2_approx(s.ref[v][n] - top);
+        total += s.ref[v][n] == top ? s.sum[v][n] : s.sum[v][n] * ver_exp2(s.ref[v][n] - top);
       constexpr int kPer = D / 32;
       float v[kPer];
       const int first_nan = s.nan_at[lane * kPer / kKv4Group];

@@ -96,11 +96,6 @@ __device__ inline bool turn_wait(TBars& s, uint32_t* p, uint32_t v, int32_t* err
   return __all_sync(0xffffffffu, x == v);
 }
 
-__device__ inline float ex2a(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ inline void fma2(float& x, float& y, float a, float b) {  // x, y = x * a + b, y * a + b
   asm("{\n\t.reg .b64 u, v, w;\n\t"
       "mov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %2};\n\tmov.b64 w, {%3, %3};\n\t"
@@ -115,12 +110,6 @@ __device__ inline void add2(float& x, float& y, float a, float b) {
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
 }
-__device__ inline uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Column position n of the K / V tiles holds dim dim_of(n): see the conversion.
 template <int D>
 __device__ constexpr int dim_of(int n) {
@@ -398,8 +387,8 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
           for (int u = 0; u < 8; ++u) x[u] = 0.f;
           if (real) Elem<__nv_bfloat16>::to_f32(ld_nc_v4(src + dim_of<D>(8 * c8)), x);
           *reinterpret_cast<uint4*>(qbuf + (c8 >> 3) * kHalf + m * 128 + (((c8 & 7) ^ (m & 7)) << 4)) =
-              make_uint4(pack_half2(x[0] * down, x[1] * down), pack_half2(x[2] * down, x[3] * down),
-                         pack_half2(x[4] * down, x[5] * down), pack_half2(x[6] * down, x[7] * down));
+              make_uint4(ver_half2(x[0] * down, x[1] * down), ver_half2(x[2] * down, x[3] * down),
+                         ver_half2(x[4] * down, x[5] * down), ver_half2(x[6] * down, x[7] * down));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -440,10 +429,10 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
               }
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                x[e] = ex2a(x[e]);
-                x[e + 1] = ex2a(x[e + 1]);
+                x[e] = ver_exp2(x[e]);
+                x[e + 1] = ver_exp2(x[e + 1]);
                 add2(acc[e & 2], acc[(e & 2) + 1], x[e], x[e + 1]);
-                w[e / 2] = pack_half2(x[e], x[e + 1]);
+                w[e / 2] = ver_half2(x[e], x[e + 1]);
               }
               tmem_st16u(pp + 16 * b, w);
             }
@@ -466,7 +455,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
               for (int e = 0; e < 32; ++e) mx = fmaxf(mx, 32 * b + e < seen ? x[e] * f : -INFINITY);
             }
             const float next = move && mx > now + kTRoom ? mx - kTRoom : now;
-            if (next != ref) sum *= ex2a(ref - next);
+            if (next != ref) sum *= ver_exp2(ref - next);
             ref = next;
             if ((c > 0 || h > 0) && __any_sync(0xffffffffu, next != now)) {
               // O holds the keys before these, once their P V has landed
@@ -475,7 +464,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
               if (ok && h == 1) ok = ver_wait_warp(s, &s.h_done, uint32_t(k) & 1, a.err);
               if (!ok) break;
               tc_fence_after();
-              const float al = next == now ? 1.f : ex2a(now - next);
+              const float al = next == now ? 1.f : ver_exp2(now - next);
 #pragma unroll 1
               for (int h2 = 0; h2 < D / 32; ++h2) {
                 float ov[32];
@@ -512,7 +501,7 @@ __global__ void __launch_bounds__(kTThreads, 1) verify_tc_kernel(const VerArgs a
       if (!ver_wait_warp(s, &s.joined[wp], uint32_t(piece) & 1, a.err)) break;
       const float2 other = s.state[piece & 1][grp ^ 1][m];
       const float last = fmaxf(ref, other.y);
-      sum = (ref == last ? sum : sum * ex2a(ref - last)) + (other.y == last ? other.x : other.x * ex2a(other.y - last));
+      sum = (ref == last ? sum : sum * ver_exp2(ref - last)) + (other.y == last ? other.x : other.x * ver_exp2(other.y - last));
       if (!ver_wait_warp(s, &s.o_full, uint32_t(piece) & 1, a.err)) break;
       tc_fence_after();
       const bool whole = p.c0 == 0 && p.c1 == p.n;
