@@ -27,7 +27,7 @@ __device__ inline Kv4Row kv4_row(unsigned char* block, int page_size, int D, int
   return r;
 }
 
-// Two e2m1 codes (one byte) as fp16 values, low half first. 64-bit forms of eight codes below.
+// Eight e2m1 codes as fp16 values, the low half of each byte first.
 __device__ inline void e2m1x8_to_half2(uint32_t w, uint32_t* h) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "mov.b32 {a, b, c, d}, %4;\n\t"

@@ -15,7 +15,13 @@ namespace ls {
 
 constexpr int kVerChunk = 128;   // keys per chunk
 constexpr int kVerMaxSms = 160;  // CTA slots are sized for at most this many SMs
-constexpr int kMmaMostRows = 24;  // query rows per KV head up to which the warp-level kernel runs
+// Query rows per KV head up to which the warp-level kernel runs, the tcgen05 kernel above. Both
+// measured, 8 KV heads of 128, 16 requests at 56K / at 4K, us: 16 rows 488 / 69, 20 rows 634 / 72 against
+// 557 / 82, 24 rows 636 / 74 against 565 / 83, 32 rows (four row tiles) 969 / 106 against 592 / 86. Head dim
+// 64, 4 KV heads, at 56K: 24 rows 253 against 277, 32 rows 326 against 285. From 17 to 24 rows the faster
+// one depends on the lengths, which the host does not see: the warp-level kernel loses 14 % or wins
+// 12; above them it loses 14 to 70 %.
+constexpr int kMmaMostRows = 24;
 // its CTAs per SM: registers hold 3 with up to 8 rows (shared memory as well), then 2 and 1
 __host__ __device__ constexpr int mma_ctas(int rows) { return rows <= 8 ? 3 : (rows <= 16 ? 2 : 1); }
 constexpr int kTcRows = 128;      // MR of the tcgen05 kernel: a state's query rows per KV head are at most 128
@@ -83,7 +89,7 @@ struct VerPiece {
   int64_t c0, c1, n, len;
 };
 
-// Whole warp. total: chunks of all tiles.
+// Whole warp: where CTA `cta` begins in the line, and its range's length (0 where it has none).
 __device__ inline VerCursor ver_begin(const VerArgs& a, int cta) {
   VerCursor u{0, 0, 0, 0};
   const int lane = threadIdx.x & 31;

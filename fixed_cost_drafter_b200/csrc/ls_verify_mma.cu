@@ -1,10 +1,13 @@
 // ls_verify_attend_kv4 for few query rows per KV head (decoding, short blocks) of bf16 states.
 //
-// Measured: decoding 16 requests at 48K-64K tokens, 1.06 GB of cache: 230 us, 4.6 TB/s (70 % of
+// Measured: decoding 16 requests at 48K-64K tokens, 1.06 GB of cache: 235 us, 4.5 TB/s (69 % of
 // the copy rate). The work is to turn 4-bit codes into fp16 MMA operands as fast as the bytes
-// arrive: about 2200 warp instructions per 128 keys, half of them conversions and scalings, at
-// 0.57 a cycle and sub-partition bound it (four CTAs per SM with two stages each, 96 registers:
-// the same; five: 295 us). The operands are made in registers, from shared
+// arrive: about 2200 warp instructions per 128 keys, half of them conversions and scalings, issued
+// in 57 % of the cycles. No unit is full (ALU 52 %, DRAM 70 %); what holds a step is latency with few
+// warps to cover it: 3.4 warps per sub-partition, and of the 6.0 cycles that a warp spends per
+// instruction 1.5 wait for the result before it, 0.8 for other warps' turns, 0.7 for memory, 0.6 for a
+// busy pipe. (Four CTAs per SM with two stages each, 96 registers: the same; five: 295 us.)
+// The operands are made in registers, from shared
 // memory that bulk copies fill (a page's block of one KV head is one contiguous copy), and
 // never go back to shared memory: warp-level m16n8k16 products, whose M = 16 side is the
 // cache (16 keys, then 16 output dimensions) and whose N = 8 side the query rows.

@@ -96,11 +96,14 @@ extern "C" {
 #define LS_VIEW_ALL      0x7
 /* Launch hint for ls_draft_attend_views, OR-ed into `views`: the call's queries and
  * boundary rows were complete before the kernel launched just before this call on
- * `stream` started, and that kernel neither reads nor writes d_out (e.g. the drafter's
- * queries of every layer came from one earlier ls_draft_prologue, and the attention is
- * called layer by layer). The attention may then read those inputs, and write d_out,
- * while that kernel still runs, so consecutive per-layer calls overlap. A hint that
- * does not hold gives wrong outputs (never a fault).                                  */
+ * `stream` started, and no kernel that may still run reads or writes d_out: not that kernel,
+ * nor, if a call with the hint launched it, those of the calls with the hint before it and the
+ * one before the first of them (e.g. the drafter's queries of every layer came from one
+ * earlier ls_draft_prologue, and the attention is called layer by layer, each layer into an
+ * output of its own). The attention may then read those inputs, and write d_out, while
+ * kernels before it still run, so consecutive per-layer calls overlap. What is launched
+ * behind them waits for all of them. A hint that does not hold gives wrong outputs (never
+ * a fault).                                                                           */
 #define LS_ATTEND_INPUTS_READY 0x100
 
 /* ---- dtypes and flags -------------------------------------------------------- */
@@ -471,6 +474,11 @@ LS_API int ls_pages_trim(ls_state* st, const ls_page_pool* h_pool, const int64_t
  * the even code; 0 where s is 0), and it stands for code * s, which bf16 holds exactly. That
  * is 4.5 bits an element. A group with an infinite or NaN element gets the scale NaN: all of
  * it reads as NaN.
+ * There is no second scale per layer or head, so a group's largest element should lie between
+ * 0.094 and 2688: below 6 * 2^-6 = 0.094 the scale is a multiple of 2^-9 with fewer bits, up to
+ * 6 * 2^-10 = 0.0059 it is 0 and the group reads as zeros, and elements beyond 6 * 448 = 2688
+ * read as 2688. Rows of other sizes are scaled by the caller: keys before the append, with the
+ * inverse in softmax_scale or in the queries; values before it, with the inverse on the output.
  * Host struct, passed by pointer; the pointers in it are DEVICE memory owned by the caller.
  *   layers[l]   base of the target's layer l: page p at layers[l] + p * page_stride (bytes;
  *               16-byte aligned, page_stride a multiple of 16 and >= ls_kv4_page_bytes). All of
@@ -508,7 +516,9 @@ LS_API int ls_kv4_append(ls_state* st, const ls_paged_kv4* h_kv, int32_t layer, 
                          int64_t row_stride, const int64_t* d_slots, int64_t n_rows, cudaStream_t stream);
 
 /* Reads rows back as `dtype` values (exact in bf16): what the attention over this cache
- * sees, e.g. as the verify rows of ls_commit_round. Layouts as ls_kv4_append; a row whose
+ * sees, e.g. as the verify rows of ls_commit_round: a call per sequence and layer, since a
+ * call's rows lie one row_stride apart and a sequence's rows of a layer follow one another in
+ * [b][L][B+1][Hkv][D]. Layouts as ls_kv4_append; a row whose
  * slot is -1 is left as it was, any other slot outside the pool sets LS_DEVERR_PAGE and
  * leaves it too.                                                                         */
 LS_API int ls_kv4_read_rows(ls_state* st, const ls_paged_kv4* h_kv, int32_t layer, const int64_t* d_slots,
