@@ -2,8 +2,9 @@
 // for the format. Both kernels move each element once and are bound by those bytes: a thread
 // takes the 16 bytes of a row's elements that make one full-width load or store (8 bf16 or 4 fp32
 // elements of a key, and the value's), the 2 or 4 threads of a scale group share its maximum.
-// 64K rows of 8 heads x 128 written (87 us) and read (67 us): 153 us together, 4.5 TB/s, 69 % of
-// the copy rate (a thread per scale group with divisions: 200 us).
+// 64K rows of 8 heads x 128 written (85 us) and read (70 us): 153 us together, 4.5 TB/s, 69 % of
+// the copy rate (a thread per scale group with divisions: 200 us). fp32 rows: written 172 us (3.6 TB/s,
+// a division per element), read 129 us (4.8 TB/s).
 #include "ls_kv4.cuh"
 
 namespace ls {
