@@ -1,6 +1,6 @@
 // ls_verify_attend_kv4 for few query rows per KV head (decoding, short blocks) of bf16 states.
 //
-// Measured: decoding 16 requests at 48K-64K tokens, 1.06 GB of cache: 235 us, 4.5 TB/s (69 % of
+// Measured: decoding 16 requests at 48K-64K tokens, 1.06 GB of cache: 230 to 238 us, 4.5 TB/s (69 % of
 // the copy rate). The work is to turn 4-bit codes into fp16 MMA operands as fast as the bytes
 // arrive: about 2200 warp instructions per 128 keys, half of them conversions and scalings, issued
 // in 57 % of the cycles. No unit is full (ALU 52 %, DRAM 70 %); what holds a step is latency with few

@@ -1,7 +1,7 @@
 // ls_verify_attend_kv4 for many query rows per KV head (a verification pass's B + 1 rows of a
 // GQA group) of bf16 states, on the 5th-generation tensor cores.
 //
-// Measured: 16 requests x 17 rows (68 rows per KV head) at 32K-64K tokens, 906 MB of cache: 525 to
+// Measured: 16 requests x 17 rows (68 rows per KV head) at 32K-64K tokens, 906 MB of cache: 520 to
 // 550 us over runs (1.7 TB/s), 13.9 ms on CUDA cores. What bounds it: instructions and the
 // latencies between roles. The two products of a 128-key chunk (128 rows x 128 keys x D each)
 // need 1024 cycles, its bytes about 760 at the copy rate, its weights' exponentials 1024 (68 rows
